@@ -250,6 +250,86 @@ mag_status mag_prefill_batch(mag_ctx* ctx, int32_t n_sessions, const int32_t* se
 mag_status mag_verify_tokens(mag_ctx* ctx, int32_t session, int32_t n_tokens, const void* hidden_in_dev,
                              void* out_dev);
 
+/* ---- the pieces of a decoding loop outside the built-in step ----
+ * For layers that the built-in step does not have (another norm, adapters, experts): the caller runs its own
+ * projections, and takes from the library the cache and what reads it. Per chunk of new tokens (one each for a decode
+ * step): mag_session_extend once, then per layer mag_kv_write and mag_attend, and mag_sample on the logits of the
+ * caller's own head or of mag_decode_step. The pages have no counterpart of their own: the cache is the block
+ * pool of [Core] 5.2 with the precisions of [Core] 5.4.
+ *
+ * The calls take up to 16 distinct sessions, whatever max_batch is, and session i's n_tokens_host[i] NEWEST tokens
+ * (0 .. its length; 0: the session is left out): its rows in the caller's buffers follow those of session i - 1,
+ * oldest token first. They share positions, blocks and lengths with every other call on the session. The
+ * rows are fp16, buffers 16-byte aligned; `ld` is the number of values from one row to the next (a multiple of 8, so a
+ * part of a wider row, such as merged q, k and v, can be passed as it lies). The context's device must be
+ * current. Stream-ordered; nothing is launched on error. The calls may be captured on the context's stream into a
+ * CUDA graph (sessions, counts and lengths are then those of the capture; make one mag_attend of the same
+ * shape before it, which allocates its workspace); replays are ordered like the calls, one after another. */
+
+/* Make room for new tokens: session i grows by n_tokens_host[i] >= 0 tokens at its next positions, whose keys and
+ * values are undefined in every layer until they are written (mag_kv_write). All sessions or none. Block-table
+ * entries are copied to the device in stream order. Errors: INVALID_ARG, CONTEXT_FULL, KV_FULL, OOM, CUDA. */
+mag_status mag_session_extend(mag_ctx* ctx, int32_t n_sessions, const int32_t* session_ids_host,
+                              const int32_t* n_tokens_host);
+
+/* Store already-rotated keys and values [rows][n_kv_heads][head_dim] of one layer for the sessions' newest tokens,
+ * quantised as they are written to the same bytes as by mag_kv_append. Tokens may be written again. The values of an
+ * INT8 or INT4 pool must be finite. k_dev and v_dev have the same row stride. Errors: INVALID_ARG, CUDA. */
+mag_status mag_kv_write(mag_ctx* ctx, int32_t layer, int32_t n_sessions, const int32_t* session_ids_host,
+                        const int32_t* n_tokens_host, const void* k_dev, const void* v_dev, int64_t ld);
+
+/* Read the same rows back as fp16: the stored value (FP16), fp16(s q) (INT8) or fp16(s q + m) (INT4), one rounding.
+ * Errors: INVALID_ARG, CUDA. */
+mag_status mag_kv_read(mag_ctx* ctx, int32_t layer, int32_t n_sessions, const int32_t* session_ids_host,
+                       const int32_t* n_tokens_host, void* k_dev, void* v_dev, int64_t ld);
+
+/* Read tokens first .. first + n_tokens - 1 of one session back in every layer, [n_layers][n_tokens][n_kv_heads]
+ * [head_dim] fp16 each: the counterpart of mag_kv_append, to move a session out of the pool. Of an FP16 pool an append
+ * of the result restores the cache exactly; of an INT8 or INT4 pool it quantises the rounded values once more.
+ * Errors: INVALID_ARG, CUDA. */
+mag_status mag_kv_export(mag_ctx* ctx, int32_t session, int32_t first, int32_t n_tokens, void* k_dev, void* v_dev);
+
+/* Causal grouped-query attention of the sessions' newest tokens over one layer of the pool:
+ *   out[r][h] = sum_j softmax_j(scale q[r][h] . k_j) v_j,   h reading KV head h / (n_heads / n_kv_heads),
+ * over the keys j <= p of a token at position p, and j > p - window when window > 0 (0: no window); k and v are the
+ * fp16 values that mag_kv_read gives. q_dev is fp16 [rows][n_heads][head_dim] (already rotated), row stride ldq;
+ * out_dev the same with row stride ldo; the two must not overlap. The sums, the softmax and its maximum are kept in fp32. A row's result does
+ * not depend on the other sessions of the call beyond how its keys are split over blocks. Stored values must be
+ * finite where any of the call's tokens, windowed or not, could lie near them (a product with 0 of an infinite
+ * value is NaN); slots past a session's end may hold anything. scale must be finite.
+ * Errors: INVALID_ARG, OOM (the workspace), CUDA. */
+mag_status mag_attend(mag_ctx* ctx, int32_t layer, int32_t n_sessions, const int32_t* session_ids_host,
+                      const int32_t* n_tokens_host, const void* q_dev, int64_t ldq, void* out_dev, int64_t ldo,
+                      int32_t window, float scale);
+
+typedef enum { MAG_LOGITS_F16 = 0, MAG_LOGITS_F32 = 1 } mag_logits_type;
+
+/* Settings of mag_sample, device arrays with one value per row; a null array turns its setting off (temperature: 1).
+ * Every value means something: temperature <= 0 (or NaN) takes the largest logit; top_k <= 0, top_p >= 1 and
+ * min_p <= 0 are off; top_p <= 0 and min_p > 1 keep one token. */
+typedef struct mag_sample_params {
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  const uint32_t* allowed; /* [rows][ceil(vocab / 32)]: bit i & 31 of word i >> 5 says that token i may be drawn */
+} mag_sample_params;
+
+/* Draw one token per row of logits [rows][vocab] (row stride ld values; fp16 or fp32) from given uniform numbers in
+ * [0, 1). Stateless; ordered on `cuda_stream`, of the current device. With the tokens in order of falling logits,
+ * equal ones by rising index, and w_i = exp((l_i - max) / temperature):
+ *   top_k keeps the first k tokens; top_p the shortest prefix whose w add up to at least top_p of the sum over what
+ *   top_k kept; min_p the tokens with w >= min_p (the first always); what all three keep is a prefix, and the
+ *   token is the first whose running sum of w exceeds u times the prefix's sum.
+ * Sums are exact in integers (w in units of 2^-40), so a result depends on nothing but its row. token_dev[row] is
+ * the token's index, -1 for a row with no token to draw (none allowed, or every logit NaN or -inf; those are never
+ * drawn); prob_dev[row] (may be null) its share of the kept w, NaN for a row without a token. Infinite
+ * logits share all the weight. p may be null (temperature 1, no cuts).
+ * Errors: INVALID_ARG, UNSUPPORTED (vocab above 614,400 in fp16, 307,200 in fp32), CUDA. */
+mag_status mag_sample(const void* logits_dev, int32_t logits_type, int32_t rows, int32_t vocab, int64_t ld,
+                      const mag_sample_params* p, const float* uniform_dev, int32_t* token_dev, float* prob_dev,
+                      void* cuda_stream);
+
 /* Wait for the context's stream and read the device error word
  * (MAG_ERR_TIMEOUT if a bounded device wait gave up). */
 mag_status mag_sync(mag_ctx* ctx);

@@ -25,11 +25,13 @@ W_QKV, W_O, W_GATE_UP, W_DOWN, NORM_ATTN, NORM_FFN, NORM_FINAL, LM_HEAD = range(
 FMT_F32_DENSE, FMT_W4G32, FMT_F16 = 0, 1, 2
 FLAG_NO_GRAPH, FLAG_ARENA_NO_REUSE, FLAG_NO_PDL, FLAG_ELASTIC_POOL, FLAG_STEP_TIMING = 1, 2, 4, 8, 16
 FLAG_DEBUG_CANARY = 32
+LOGITS_F16, LOGITS_F32 = 0, 1
 
 EXPORTED = [
     "mag_create", "mag_destroy", "mag_load_weights", "mag_load_weights_f32_noalloc", "mag_session_open", "mag_session_close", "mag_session_length",
     "mag_session_truncate", "mag_kv_append", "mag_decode_step", "mag_decode_step_host", "mag_prefill_chunk",
     "mag_verify_tokens", "mag_prefill_batch", "mag_sync",
+    "mag_session_extend", "mag_kv_write", "mag_kv_read", "mag_kv_export", "mag_attend", "mag_sample",
     "mag_get_memory_stats", "mag_get_step_stats", "mag_last_error", "mag_kv_bytes_per_token", "mag_quantize_w4g32",
     "mag_debug_read_weights", "mag_debug_kv_locate", "mag_debug_pool", "mag_debug_arena_plan",
     "mag_debug_last_step_launches", "mag_debug_profile_step", "mag_debug_step_residuals", "mag_debug_timeline",
@@ -84,6 +86,11 @@ class ArenaTensor(ctypes.Structure):
                 ("last", ctypes.c_int32), ("offset", ctypes.c_uint64)]
 
 
+class SampleParams(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+                ("min_p", ctypes.c_void_p), ("allowed", ctypes.c_void_p)]
+
+
 class AdaptConfig(ctypes.Structure):
     _fields_ = [("enable_adaptive", ctypes.c_int32), ("adaptive_window_size", ctypes.c_int32),
                 ("adaptive_sample_rate", ctypes.c_int32), ("plan_short_below", ctypes.c_int32),
@@ -131,6 +138,12 @@ def lib():
                 "mag_verify_tokens": ([vp, i32, i32, vp, vp], i32),
                 "mag_prefill_batch": ([vp, i32, P32, P32, vp, vp], i32),
                 "mag_sync": ([vp], i32),
+                "mag_session_extend": ([vp, i32, P32, P32], i32),
+                "mag_kv_write": ([vp, i32, i32, P32, P32, vp, vp, i64], i32),
+                "mag_kv_read": ([vp, i32, i32, P32, P32, vp, vp, i64], i32),
+                "mag_kv_export": ([vp, i32, i32, i32, vp, vp], i32),
+                "mag_attend": ([vp, i32, i32, P32, P32, vp, i64, vp, i64, i32, ctypes.c_float], i32),
+                "mag_sample": ([vp, i32, i32, i32, i64, ctypes.POINTER(SampleParams), vp, vp, vp, vp], i32),
                 "mag_get_memory_stats": ([vp, ctypes.POINTER(MemoryStats)], i32),
                 "mag_get_step_stats": ([vp, ctypes.POINTER(StepStats)], i32),
                 "mag_last_error": ([vp], ctypes.c_char_p),
@@ -204,6 +217,17 @@ def quantize_w4g32(src, rows, cols, codes, scale_min, stream=0):
         raise MagError(st, "mag_quantize_w4g32")
 
 
+def sample(logits, rows, vocab, uniform, token, prob=None, ld=None, dtype=LOGITS_F16, temperature=None, top_k=None,
+           top_p=None, min_p=None, allowed=None, stream=0):
+    """Draw token[rows] (int32) from logits [rows, vocab] (row stride ld, vocab by default); the settings are device
+    arrays with one value per row (temperature, top_p, min_p fp32, top_k int32), allowed [rows, ceil(vocab / 32)]."""
+    p = SampleParams(_ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(allowed))
+    st = lib().mag_sample(_ptr(logits), dtype, rows, vocab, vocab if ld is None else ld, ctypes.byref(p),
+                          _ptr(uniform), _ptr(token), _ptr(prob), stream)
+    if st != OK:
+        raise MagError(st, "mag_sample")
+
+
 def adapt_defaults() -> AdaptConfig:
     a = AdaptConfig()
     lib().mag_adapt_defaults(ctypes.byref(a))
@@ -251,6 +275,14 @@ def plan_for(p90, short_below=128, long_above=512) -> int:
 
 def hot_pool_blocks(p90, n_sessions, slack=1.2) -> int:
     return int(lib().mag_hot_pool_blocks(p90, n_sessions, slack))
+
+
+def _lists(sessions, n_tokens):
+    """(count, session ids, token counts) as the C calls take them."""
+    if len(sessions) != len(n_tokens):
+        raise ValueError(f"{len(sessions)} sessions but {len(n_tokens)} token counts")
+    n = len(sessions)
+    return n, (ctypes.c_int32 * n)(*sessions), (ctypes.c_int32 * n)(*n_tokens)
 
 
 class Context:
@@ -330,6 +362,34 @@ class Context:
 
     def verify_tokens(self, sid, n_tokens, hidden_in, out):
         self._check(lib().mag_verify_tokens(self.h, sid, n_tokens, _ptr(hidden_in), _ptr(out)), "mag_verify_tokens")
+
+    def session_extend(self, sessions, n_tokens):
+        """Make room for n_tokens[i] new tokens of every session (written later, layer by layer)."""
+        self._check(lib().mag_session_extend(self.h, *_lists(sessions, n_tokens)), "mag_session_extend")
+
+    def kv_write(self, layer, sessions, n_tokens, k, v, ld=None):
+        """Keys and values [rows, n_kv_heads, head_dim] of the sessions' newest tokens into one layer of the pool."""
+        ld = self.cfg.n_kv_heads * self.cfg.head_dim if ld is None else ld
+        self._check(lib().mag_kv_write(self.h, layer, *_lists(sessions, n_tokens), _ptr(k), _ptr(v), ld),
+                    "mag_kv_write")
+
+    def kv_read(self, layer, sessions, n_tokens, k, v, ld=None):
+        """The same rows back, as fp16."""
+        ld = self.cfg.n_kv_heads * self.cfg.head_dim if ld is None else ld
+        self._check(lib().mag_kv_read(self.h, layer, *_lists(sessions, n_tokens), _ptr(k), _ptr(v), ld),
+                    "mag_kv_read")
+
+    def kv_export(self, sid, first, n_tokens, k, v):
+        """Tokens first .. of one session in every layer, fp16 [n_layers, n_tokens, n_kv_heads, head_dim] each."""
+        self._check(lib().mag_kv_export(self.h, sid, first, n_tokens, _ptr(k), _ptr(v)), "mag_kv_export")
+
+    def attend(self, layer, sessions, n_tokens, q, out, ldq=None, ldo=None, window=0, scale=None):
+        """Causal attention of the sessions' newest tokens, q and out [rows, n_heads, head_dim], over one layer of
+        the pool (scale: head_dim ** -0.5 by default)."""
+        width = self.cfg.n_heads * self.cfg.head_dim
+        scale = self.cfg.head_dim ** -0.5 if scale is None else scale
+        self._check(lib().mag_attend(self.h, layer, *_lists(sessions, n_tokens), _ptr(q), width if ldq is None else ldq,
+                                     _ptr(out), width if ldo is None else ldo, window, scale), "mag_attend")
 
     def sync(self):
         self._check(lib().mag_sync(self.h), "mag_sync")

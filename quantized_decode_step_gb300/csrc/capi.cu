@@ -48,6 +48,7 @@ mag_status check_err(mag_ctx* c) {
   }
   cudaMemsetAsync(c->d_counters, 0, c->n_counters * 4, c->stream);
   cudaMemsetAsync(c->attn_arrivals, 0, (size_t)c->B_max * c->Hkv * 4, c->stream);
+  if (c->at_arrivals) cudaMemsetAsync(c->at_arrivals, 0, (size_t)kAttendMaxSplitBlocks * 4, c->stream);
   if (c->pf_part_cnt) cudaMemsetAsync(c->pf_part_cnt, 0, (size_t)(c->n_sm / 2) * 4 * 4, c->stream);
   return fail(c, MAG_ERR_TIMEOUT, "a kernel's pipeline wait gave up (code 0x%x)", e);
 }
@@ -325,6 +326,9 @@ void free_ctx(mag_ctx* c) {
   cudaFree(c->pf_part);
   cudaFree(c->pf_part_cnt);
   cudaFree(c->pf_last_r);
+  cudaFree(c->at_part);
+  cudaFree(c->at_ml);
+  cudaFree(c->at_arrivals);
   if (c->own_stream && c->stream) cudaStreamDestroy(c->stream);
   delete c;
 }

@@ -181,6 +181,10 @@ struct mag_ctx {
   float* pf_part = nullptr;     // split-K GEMMs: partial sums of the two K halves
   uint32_t* pf_part_cnt = nullptr;
   float* pf_last_r = nullptr;   // [MAG_MAX_BATCH][D]: the sessions' last residual rows, gathered
+  // mag_attend's workspace (split tiles), allocated by the first call that splits
+  float* at_part = nullptr;
+  float* at_ml = nullptr;
+  uint32_t* at_arrivals = nullptr;
   alignas(64) uint8_t map_xn[128];
   alignas(64) uint8_t map_o[128];
   alignas(64) uint8_t map_act[128];
@@ -249,5 +253,9 @@ mag_status stats_end(mag_ctx* c);  // launches from last_launches; the end event
 mag_status setup_prefill(mag_ctx* c);
 mag_status run_chunk(mag_ctx* c, const char* what, int n_seg, const int32_t* sids, const int32_t* ntok,
                      const void* in, void* out, bool all_rows, float* resid_dump = nullptr);
+
+// ops.cu
+mag_status run_attend(mag_ctx* c, int32_t layer, const KvRows& rows, const void* q, int64_t ldq, void* out, int64_t ldo,
+                      int32_t window, float scale);
 
 }  // namespace mag

@@ -243,6 +243,87 @@ constexpr int kAttnMaxGroups = 8;
 // Largest split count (cluster size) the device can co-schedule for this head size, KV type and variant.
 cudaError_t attention_max_cluster(int head_dim, int kv_dtype, bool wide, int* out);
 
+// ---------------------------------------------------------------- a layer's cache and attention as calls
+// The newest tokens of up to 16 sessions: session i's n_tok tokens from position pos0 are rows row0 .. of the
+// caller's buffers, the sessions following each other.
+struct KvSeg {
+  int32_t row0, n_tok, pos0, sess;
+};
+struct KvRows {
+  int32_t n_seg, n_rows;
+  KvSeg seg[MAG_MAX_BATCH];
+};
+struct KvWriteArgs {
+  const __half* k;  // row r's heads at k + r ld
+  const __half* v;
+  int64_t ld;
+  int32_t layer;
+  KvRows rows;
+  PoolGeom pool;
+  uint32_t* err;  // kErrBounds when a table entry is outside the pool
+};
+cudaError_t launch_kv_write(const Launch& L, const KvWriteArgs& a);
+struct KvReadArgs {
+  __half* k;  // row r of layer `layer` + z at k + z layer_stride + r ld
+  __half* v;
+  int64_t ld, layer_stride;
+  int32_t layer;
+  int32_t n_blocks;              // pool blocks that the rows touch
+  int32_t blk0[MAG_MAX_BATCH];   // first of them of each session
+  KvRows rows;
+  PoolGeom pool;
+  uint32_t* err;
+};
+cudaError_t launch_kv_read(const Launch& L, const KvReadArgs& a, int n_layers);
+
+// Causal grouped-query attention of the sessions' newest tokens over the pool. The G query heads of a KV head and
+// the tokens of a session are packed into rows, row t G + g, cut into tiles; a tile's keys may be split over
+// several blocks, which leave (m, l, o) in the workspace for the last of them to merge.
+struct AttendSeg {
+  int32_t row0, n_tok, pos0, sess;  // as KvSeg
+  int32_t unit0;                    // first block of this session
+  int32_t n_split, n_tiles;         // blocks: ((tile * Hkv) + head) * n_split + split
+  int32_t slot0, part0;             // split: first (tile, head) in the workspace's counters, first block in its parts
+};
+struct AttendArgs {
+  const __half* q;  // token row r, head h at q + r ldq + h d
+  int64_t ldq;
+  __half* o;
+  int64_t ldo;
+  int32_t n_heads, n_kv_heads, group, layer;
+  int32_t window;   // 0: every key up to the token's own
+  float scale_log2; // scale * log2(e)
+  float* part;      // split tiles: per block [tile rows][d] of o, fp32
+  float* part_ml;   // per block [tile rows][2]: running maximum (log2 units) and sum
+  uint32_t* arrivals;  // per (tile, head), zero between launches
+  int32_t n_seg, n_units;
+  AttendSeg seg[MAG_MAX_BATCH];
+  PoolGeom pool;
+  uint32_t* err;
+};
+// Few rows: tiles of 8 or 16 rows.
+constexpr int kAttendMaxSplitBlocks = 2048;  // blocks of one launch that may leave partial results
+constexpr size_t kAttendPartRows = (size_t)kAttendMaxSplitBlocks * 16, kAttendPartFloats = kAttendPartRows * 128;
+cudaError_t launch_attend_few(const Launch& L, const AttendArgs& a, int tile_rows);
+
+// ---------------------------------------------------------------- sampling
+struct SampleArgs {
+  const void* logits;  // row r at logits + r ld values
+  int64_t ld;
+  int32_t rows, vocab;
+  int32_t f32;         // logits in fp32 (else fp16)
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  const float* uniform;
+  const uint32_t* allowed;  // [rows][ceil(vocab / 32)]
+  int32_t* token;
+  float* prob;
+};
+cudaError_t launch_sample(cudaStream_t s, const SampleArgs& a);
+int64_t sample_max_vocab(bool f32);  // largest vocabulary that a cluster holds
+
 // ---------------------------------------------------------------- W4 quantiser (load time)
 cudaError_t launch_quantize_w4g32(cudaStream_t s, const float* src, int64_t rows, int64_t cols, uint8_t* codes,
                                   __half2* sm);

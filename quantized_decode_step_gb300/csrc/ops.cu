@@ -1,0 +1,304 @@
+// The pieces of a decoding loop outside the built-in step: session extension, one layer's cache write, read-back
+// and attention over a context's pool, and sampling.
+#include "engine.h"
+
+namespace mag {
+
+// The rows of a call: session sids[i]'s newest ntok[i] tokens, sessions without any left out. Errors leave `r`
+// unspecified.
+static mag_status op_rows(mag_ctx* c, const char* what, int32_t layer, int32_t n, const int32_t* sids,
+                          const int32_t* ntok, KvRows& r) {
+  r = KvRows{};
+  if (n < 1 || n > MAG_MAX_BATCH)
+    return fail(c, MAG_ERR_INVALID_ARG, "%s: %d sessions not in 1..%d", what, n, MAG_MAX_BATCH);
+  if (!sids || !ntok) return fail(c, MAG_ERR_INVALID_ARG, "%s: null session or token list", what);
+  if (layer < 0 || layer >= c->L) return fail(c, MAG_ERR_INVALID_ARG, "%s: bad layer %d", what, layer);
+  int64_t rows = 0;
+  for (int i = 0; i < n; ++i) {
+    const int sid = sids[i];
+    if (sid < 0 || sid >= (int)c->sessions.size() || !c->sessions[sid].open)
+      return fail(c, MAG_ERR_INVALID_ARG, "%s: session %d is not open", what, sid);
+    for (int j = 0; j < i; ++j)
+      if (sids[j] == sid) return fail(c, MAG_ERR_INVALID_ARG, "%s: session %d appears twice", what, sid);
+    const Session& s = c->sessions[sid];
+    if (ntok[i] < 0 || ntok[i] > s.len)
+      return fail(c, MAG_ERR_INVALID_ARG, "%s: %d tokens of session %d, which holds %d", what, ntok[i], sid, s.len);
+    if (ntok[i] == 0) continue;
+    if (rows + ntok[i] > (1 << 24)) return fail(c, MAG_ERR_INVALID_ARG, "%s: more than 2^24 tokens", what);
+    r.seg[r.n_seg++] = KvSeg{(int32_t)rows, ntok[i], s.len - ntok[i], sid};
+    rows += ntok[i];
+  }
+  r.n_rows = (int32_t)rows;
+  return MAG_OK;
+}
+
+// fp16 rows of `width` values: 16-byte aligned, a row stride that is a multiple of 8 values and holds a row.
+static mag_status op_buffer(mag_ctx* c, const char* what, const char* name, const void* p, int64_t ld, int64_t width) {
+  if (!p) return fail(c, MAG_ERR_INVALID_ARG, "%s: %s is null", what, name);
+  if (reinterpret_cast<uintptr_t>(p) & 15) return fail(c, MAG_ERR_INVALID_ARG, "%s: %s is not 16-byte aligned", what, name);
+  if (ld < width || ld % 8)
+    return fail(c, MAG_ERR_INVALID_ARG, "%s: %s has row stride %lld, not a multiple of 8 of at least %lld", what, name,
+                (long long)ld, (long long)width);
+  return MAG_OK;
+}
+
+static mag_status op_device(mag_ctx* c, const char* what) {
+  int dev = -1;
+  CUDA_TRY(c, cudaGetDevice(&dev));
+  if (dev != c->device)
+    return fail(c, MAG_ERR_INVALID_ARG, "%s: make the context's device %d current (not %d)", what, c->device, dev);
+  return MAG_OK;
+}
+
+// Blocks of a read: the pool blocks that each session's tokens touch.
+static int read_blocks(const KvRows& r, int32_t* blk0) {
+  int n = 0;
+  for (int i = 0; i < r.n_seg; ++i) {
+    blk0[i] = n;
+    n += ((r.seg[i].pos0 + r.seg[i].n_tok - 1) >> 4) - (r.seg[i].pos0 >> 4) + 1;
+  }
+  return n;
+}
+
+// The workspace of split attention tiles, made by the first call that needs it.
+static mag_status attend_workspace(mag_ctx* c) {
+  if (c->at_part) return MAG_OK;
+  const size_t part = kAttendPartFloats * 4, ml = kAttendPartRows * 2 * 4, cnt = (size_t)kAttendMaxSplitBlocks * 4;
+  cudaError_t e;
+  float *p = nullptr, *m = nullptr;
+  uint32_t* n = nullptr;
+  if ((e = dev_malloc(&p, part)) != cudaSuccess || (e = dev_malloc(&m, ml)) != cudaSuccess ||
+      (e = dev_malloc(&n, cnt)) != cudaSuccess) {
+    cudaFree(p);
+    cudaFree(m);
+    return fail(c, MAG_ERR_OOM, "attend: workspace: %s", cudaGetErrorString(e));
+  }
+  if ((e = cudaMemsetAsync(n, 0, cnt, c->stream)) != cudaSuccess) {
+    cudaFree(p);
+    cudaFree(m);
+    cudaFree(n);
+    return fail(c, MAG_ERR_CUDA, "attend: workspace: %s", cudaGetErrorString(e));
+  }
+  c->at_part = p;
+  c->at_ml = m;
+  c->at_arrivals = n;
+  c->other_bytes += part + ml + cnt;
+  return MAG_OK;
+}
+
+// The sessions of a launch cut into blocks: tiles of tile_rows packed rows, each tile's keys in n_split parts so
+// that about `target` blocks come out, of no fewer than min_blocks pool blocks each.
+static void attend_units(const mag_ctx* c, AttendArgs& a, const KvRows& rows, int tile_rows, int64_t target,
+                         int min_blocks) {
+  int64_t work = 0;  // pool blocks over all tiles, with every tile at its session's length
+  for (int i = 0; i < rows.n_seg; ++i) {
+    const KvSeg& s = rows.seg[i];
+    const int64_t tiles = ((int64_t)s.n_tok * c->G + tile_rows - 1) / tile_rows;
+    int64_t keys = s.pos0 + s.n_tok;
+    if (a.window) keys = std::min<int64_t>(keys, a.window + (tile_rows + c->G - 1) / c->G);
+    work += tiles * c->Hkv * ((keys + 15) / 16);
+  }
+  const int64_t per = std::max<int64_t>(min_blocks, (work + target - 1) / target);
+  int64_t unit = 0, slot = 0, part = 0;
+  a.n_seg = rows.n_seg;
+  for (int i = 0; i < rows.n_seg; ++i) {
+    const KvSeg& s = rows.seg[i];
+    const int tiles = (int)(((int64_t)s.n_tok * c->G + tile_rows - 1) / tile_rows);
+    int64_t keys = s.pos0 + s.n_tok;
+    if (a.window) keys = std::min<int64_t>(keys, a.window + (tile_rows + c->G - 1) / c->G);
+    int split = (int)(((keys + 15) / 16 + per - 1) / per);
+    // a split tile has more than `per` blocks, so there are fewer than `target` of them and fewer than
+    // 2 target parts; whatever the arithmetic, no more than the workspace holds
+    if (split > 1 && part + (int64_t)tiles * c->Hkv * split > kAttendMaxSplitBlocks) split = 1;
+    a.seg[i] = AttendSeg{s.row0, s.n_tok, s.pos0, s.sess, (int32_t)unit, split, tiles, (int32_t)slot, (int32_t)part};
+    unit += (int64_t)tiles * c->Hkv * split;
+    if (split > 1) {
+      slot += (int64_t)tiles * c->Hkv;
+      part += (int64_t)tiles * c->Hkv * split;
+    }
+  }
+  a.n_units = (int32_t)unit;
+}
+
+mag_status run_attend(mag_ctx* c, int32_t layer, const KvRows& rows, const void* q, int64_t ldq, void* out, int64_t ldo,
+                      int32_t window, float scale) {
+  AttendArgs a = {};
+  a.q = (const __half*)q;
+  a.ldq = ldq;
+  a.o = (__half*)out;
+  a.ldo = ldo;
+  a.n_heads = c->Hq;
+  a.n_kv_heads = c->Hkv;
+  a.group = c->G;
+  a.layer = layer;
+  a.window = window;
+  a.scale_log2 = scale * 1.44269504088896340736f;
+  a.pool = pool_geom(c);
+  a.err = c->d_err;
+  int most = 0;
+  for (int i = 0; i < rows.n_seg; ++i) most = std::max(most, rows.seg[i].n_tok);
+  const int tile_rows = (int64_t)most * c->G <= 8 ? 8 : 16;
+  attend_units(c, a, rows, tile_rows, std::min(4 * c->n_sm, kAttendMaxSplitBlocks / 2), 8);
+  bool split = false;
+  for (int i = 0; i < a.n_seg; ++i) split |= a.seg[i].n_split > 1;
+  if (split) {
+    const mag_status st = attend_workspace(c);
+    if (st != MAG_OK) return st;
+  }
+  a.part = c->at_part;
+  a.part_ml = c->at_ml;
+  a.arrivals = c->at_arrivals;
+  CUDA_TRY(c, launch_attend_few(Launch{c->stream, false, nullptr}, a, tile_rows));
+  return MAG_OK;
+}
+
+}  // namespace mag
+
+extern "C" {
+
+mag_status mag_session_extend(mag_ctx* c, int32_t n, const int32_t* sids, const int32_t* ntok) {
+  if (!c) return MAG_ERR_INVALID_ARG;
+  if (n < 1 || n > MAG_MAX_BATCH)
+    return fail(c, MAG_ERR_INVALID_ARG, "session_extend: %d sessions not in 1..%d", n, MAG_MAX_BATCH);
+  if (!sids || !ntok) return fail(c, MAG_ERR_INVALID_ARG, "session_extend: null session or token list");
+  int64_t need = 0;
+  for (int i = 0; i < n; ++i) {
+    const int sid = sids[i];
+    if (sid < 0 || sid >= (int)c->sessions.size() || !c->sessions[sid].open)
+      return fail(c, MAG_ERR_INVALID_ARG, "session_extend: session %d is not open", sid);
+    for (int j = 0; j < i; ++j)
+      if (sids[j] == sid) return fail(c, MAG_ERR_INVALID_ARG, "session_extend: session %d appears twice", sid);
+    const Session& s = c->sessions[sid];
+    if (ntok[i] < 0) return fail(c, MAG_ERR_INVALID_ARG, "session_extend: %d tokens", ntok[i]);
+    if ((int64_t)s.len + ntok[i] > c->cfg.max_context)
+      return fail(c, MAG_ERR_CONTEXT_FULL, "session_extend: %d + %d tokens exceed max_context %d", s.len, ntok[i],
+                  c->cfg.max_context);
+    need += (s.len + ntok[i] + 15) / 16 - (s.len + 15) / 16;
+  }
+  const mag_status dv = op_device(c, "session_extend");
+  if (dv != MAG_OK) return dv;
+  const mag_status st = reserve_blocks(c, "session_extend", need);
+  if (st != MAG_OK) return st;
+  for (int i = 0; i < n; ++i) {
+    Session& s = c->sessions[sids[i]];
+    const int nb_old = (s.len + 15) / 16, nb_new = (s.len + ntok[i] + 15) / 16;
+    for (int b = nb_old; b < nb_new; ++b) s.table.push_back(c->kv.pop());
+    if (nb_new > nb_old)
+      CUDA_TRY(c, cudaMemcpyAsync(c->d_tables + (size_t)sids[i] * c->table_stride + nb_old, s.table.data() + nb_old,
+                                  (size_t)(nb_new - nb_old) * 4, cudaMemcpyHostToDevice, c->stream));
+    s.len += ntok[i];
+  }
+  return MAG_OK;
+}
+
+mag_status mag_kv_write(mag_ctx* c, int32_t layer, int32_t n, const int32_t* sids, const int32_t* ntok, const void* k,
+                        const void* v, int64_t ld) {
+  if (!c) return MAG_ERR_INVALID_ARG;
+  KvWriteArgs a = {};
+  mag_status st = op_rows(c, "kv_write", layer, n, sids, ntok, a.rows);
+  if (st != MAG_OK || a.rows.n_rows == 0) return st;
+  if ((st = op_buffer(c, "kv_write", "k", k, ld, (int64_t)c->Hkv * c->d)) != MAG_OK) return st;
+  if ((st = op_buffer(c, "kv_write", "v", v, ld, (int64_t)c->Hkv * c->d)) != MAG_OK) return st;
+  if ((st = op_device(c, "kv_write")) != MAG_OK) return st;
+  a.k = (const __half*)k;
+  a.v = (const __half*)v;
+  a.ld = ld;
+  a.layer = layer;
+  a.pool = pool_geom(c);
+  a.err = c->d_err;
+  CUDA_TRY(c, launch_kv_write(Launch{c->stream, false, nullptr}, a));
+  return MAG_OK;
+}
+
+mag_status mag_kv_read(mag_ctx* c, int32_t layer, int32_t n, const int32_t* sids, const int32_t* ntok, void* k, void* v,
+                       int64_t ld) {
+  if (!c) return MAG_ERR_INVALID_ARG;
+  KvReadArgs a = {};
+  mag_status st = op_rows(c, "kv_read", layer, n, sids, ntok, a.rows);
+  if (st != MAG_OK || a.rows.n_rows == 0) return st;
+  if ((st = op_buffer(c, "kv_read", "k", k, ld, (int64_t)c->Hkv * c->d)) != MAG_OK) return st;
+  if ((st = op_buffer(c, "kv_read", "v", v, ld, (int64_t)c->Hkv * c->d)) != MAG_OK) return st;
+  if ((st = op_device(c, "kv_read")) != MAG_OK) return st;
+  a.k = (__half*)k;
+  a.v = (__half*)v;
+  a.ld = ld;
+  a.layer = layer;
+  a.n_blocks = read_blocks(a.rows, a.blk0);
+  a.pool = pool_geom(c);
+  a.err = c->d_err;
+  CUDA_TRY(c, launch_kv_read(Launch{c->stream, false, nullptr}, a, 1));
+  return MAG_OK;
+}
+
+mag_status mag_kv_export(mag_ctx* c, int32_t sid, int32_t first, int32_t n, void* k, void* v) {
+  if (!c) return MAG_ERR_INVALID_ARG;
+  if (sid < 0 || sid >= (int)c->sessions.size() || !c->sessions[sid].open)
+    return fail(c, MAG_ERR_INVALID_ARG, "kv_export: session %d is not open", sid);
+  const int len = c->sessions[sid].len;
+  if (first < 0 || n < 0 || (int64_t)first + n > len)
+    return fail(c, MAG_ERR_INVALID_ARG, "kv_export: tokens %d .. + %d of a session that holds %d", first, n, len);
+  if (n == 0) return MAG_OK;
+  const int64_t ld = (int64_t)c->Hkv * c->d;
+  mag_status st = op_buffer(c, "kv_export", "k", k, ld, ld);
+  if (st == MAG_OK) st = op_buffer(c, "kv_export", "v", v, ld, ld);
+  if (st == MAG_OK) st = op_device(c, "kv_export");
+  if (st != MAG_OK) return st;
+  KvReadArgs a = {};
+  a.rows.n_seg = 1;
+  a.rows.n_rows = n;
+  a.rows.seg[0] = KvSeg{0, n, first, sid};
+  a.k = (__half*)k;
+  a.v = (__half*)v;
+  a.ld = ld;
+  a.layer_stride = n * ld;
+  a.n_blocks = read_blocks(a.rows, a.blk0);
+  a.pool = pool_geom(c);
+  a.err = c->d_err;
+  CUDA_TRY(c, launch_kv_read(Launch{c->stream, false, nullptr}, a, c->L));
+  return MAG_OK;
+}
+
+mag_status mag_attend(mag_ctx* c, int32_t layer, int32_t n, const int32_t* sids, const int32_t* ntok, const void* q,
+                      int64_t ldq, void* out, int64_t ldo, int32_t window, float scale) {
+  if (!c) return MAG_ERR_INVALID_ARG;
+  KvRows rows;
+  mag_status st = op_rows(c, "attend", layer, n, sids, ntok, rows);
+  if (st != MAG_OK) return st;
+  if (window < 0) return fail(c, MAG_ERR_INVALID_ARG, "attend: window %d", window);
+  if (!std::isfinite(scale)) return fail(c, MAG_ERR_INVALID_ARG, "attend: the scale is not finite");
+  if (rows.n_rows == 0) return MAG_OK;
+  if ((st = op_buffer(c, "attend", "q", q, ldq, (int64_t)c->Hq * c->d)) != MAG_OK) return st;
+  if ((st = op_buffer(c, "attend", "out", out, ldo, (int64_t)c->Hq * c->d)) != MAG_OK) return st;
+  if ((st = op_device(c, "attend")) != MAG_OK) return st;
+  return run_attend(c, layer, rows, q, ldq, out, ldo, window, scale);
+}
+
+mag_status mag_sample(const void* logits, int32_t type, int32_t rows, int32_t vocab, int64_t ld,
+                      const mag_sample_params* p, const float* uniform, int32_t* token, float* prob, void* stream) {
+  if (rows < 0 || vocab < 1 || ld < vocab || (type != MAG_LOGITS_F16 && type != MAG_LOGITS_F32))
+    return MAG_ERR_INVALID_ARG;
+  const bool f32 = type == MAG_LOGITS_F32;
+  if (vocab > sample_max_vocab(f32)) return MAG_ERR_UNSUPPORTED;
+  if (rows == 0) return MAG_OK;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(logits);
+  if (!logits || !uniform || !token || at % (f32 ? 4 : 2)) return MAG_ERR_INVALID_ARG;
+  SampleArgs a = {};
+  a.logits = logits;
+  a.ld = ld;
+  a.rows = rows;
+  a.vocab = vocab;
+  a.f32 = f32;
+  if (p) {
+    a.temperature = p->temperature;
+    a.top_k = p->top_k;
+    a.top_p = p->top_p;
+    a.min_p = p->min_p;
+    a.allowed = p->allowed;
+  }
+  a.uniform = uniform;
+  a.token = token;
+  a.prob = prob;
+  return launch_sample((cudaStream_t)stream, a) == cudaSuccess ? MAG_OK : MAG_ERR_CUDA;
+}
+
+}  // extern "C"
