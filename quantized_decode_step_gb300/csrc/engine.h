@@ -254,8 +254,4 @@ mag_status setup_prefill(mag_ctx* c);
 mag_status run_chunk(mag_ctx* c, const char* what, int n_seg, const int32_t* sids, const int32_t* ntok,
                      const void* in, void* out, bool all_rows, float* resid_dump = nullptr);
 
-// ops.cu
-mag_status run_attend(mag_ctx* c, int32_t layer, const KvRows& rows, const void* q, int64_t ldq, void* out, int64_t ldo,
-                      int32_t window, float scale);
-
 }  // namespace mag

@@ -58,7 +58,6 @@ struct Raw {
   static constexpr int kRow = KV == 0 ? 2 * D : (KV == 1 ? D : D / 2);  // bytes of a vector
   static constexpr int KW = kRow / 4 / 4;   // words of a key row per lane (quad shares the row)
   static constexpr int VW = kRow / 8 / 4;   // words of a value row per lane (8 lanes share the row)
-  static constexpr int MV = KV == 2 ? 1 : 0;
   uint32_t k[2][KW];   // key rows g, g + 8
   uint32_t v[4][VW];   // value rows 2t, 2t + 1, 2t + 8, 2t + 9
   uint32_t km[2];      // INT8: the row's scale (low half); INT4: (scale, min) of the lane's group

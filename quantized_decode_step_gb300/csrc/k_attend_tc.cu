@@ -1,0 +1,817 @@
+// Attention of the newest tokens of several sessions over one layer's block pool, for many rows: tcgen05.
+//
+//   o_t = sum_j softmax_j(scale q_t . k_j) v_j   over the keys j <= p_t, and j > p_t - window if there is one,
+//
+// the G query heads of a KV head and the tokens of a session packed into rows t G + g, so one read of a key serves
+// them all. What bounds it is the tensor core: 4 d flops a row and key, 2 x 128 x 128 x d a tile for Q K^T and as many for
+// P V, against 32 KB of K and V from L2.
+//
+// A unit is 256 rows (two tiles of 128) of one session and KV head over their keys in steps of 128. One block per
+// SM takes an equal share of all units' steps, in order, so that every SM works to the end whatever the causal
+// triangle leaves of the units; a unit cut by a share's end leaves (m, l, o) in the workspace, and the last of its
+// blocks to arrive adds the parts in order (the result does not depend on who was last).
+//
+// Roles: one warp loads K and V of a step into a ring of swizzled tiles (FP16 by TMA, a 16-token pool block and 64
+// dimensions a copy; INT8 and INT4 as raw bytes that four warps expand to the fp16 values the pool reads
+// back as); one thread issues the MMAs; a warpgroup per row tile takes S from tensor memory, one row a
+// thread, and leaves P there in fp16 over S's columns, where the second MMA reads it as its A operand, with V as it
+// lies (its rows are the contraction: an MN-major B operand). While one tile's softmax runs, the tensor core
+// has the other tile's P V and its next Q K^T.
+//
+// Softmax: as in the few-row kernel, base 2 with a maximum that is raised only when a score passes it by more
+// than 2^8 (the rescaling of o in tensor memory is then rare) and p scaled by 2^7 before its rounding to fp16; the sum
+// adds p in fp32 before the rounding.
+//
+// Every wait is bounded; a role whose wait gives up sets a bit in the error word and leaves, after its own copies
+// and MMAs in flight.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "kernels.h"
+
+namespace mag {
+
+namespace {
+
+constexpr int kRows = 128, kKeys = 128;  // rows of a tile, keys of a step
+constexpr float kLazy = 8.0f, kShift = 7.0f;
+constexpr uint32_t kErrAttend = 512u;
+
+__device__ __forceinline__ uint32_t su32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void mb_init(uint64_t* b, uint32_t n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(su32(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void mb_expect(uint64_t* b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mb_arrive(uint64_t* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(b)) : "memory");
+}
+__device__ __forceinline__ bool mb_wait(uint64_t* b, uint32_t par) {
+  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(su32(b)), "r"(par)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+          "r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(su32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(su32(bar))
+               : "memory");
+}
+// Shared-memory operand of 128-byte rows with 128-byte swizzle, 8-row groups 1024 bytes apart. K-major (Q, K): the
+// row is the M or N index. MN-major (V): the row is the contraction index, 64 dimensions long, and the
+// next 64 dimensions lie `next` bytes further (the leading-dimension offset).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t next) {
+  uint64_t d = (static_cast<uint64_t>(addr) & 0x3FFFFull) >> 4;
+  d |= static_cast<uint64_t>(next >> 4) << 16;
+  d |= (1024ull >> 4) << 32;
+  d |= 1ull << 46;
+  d |= 2ull << 61;
+  return d;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// 32 consecutive columns of this thread's lane, not waited for.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const float* v) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack(F2 x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ void wg_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+
+// ---------------------------------------------------------------- shapes
+template <int D, int KV>
+struct Cfg {
+  static constexpr int kTile = kKeys * D * 2;          // one K or V tile, or a Q tile, in fp16
+  static constexpr int kHalf = kKeys * 128;            // its 64-dimension halves
+  static constexpr int kStages = D == 128 ? (KV == 0 ? 5 : 4) : 8;
+  static constexpr int kRowB = KV == 0 ? 2 * D : (KV == 1 ? D : D / 2), kMetaB = KV == 0 ? 0 : (KV == 1 ? 2 : D / 8);
+  static constexpr int kRawData = kKeys * kRowB, kRawMeta = kKeys * kMetaB;
+  static constexpr int kRaw = KV == 0 ? 0 : 2;         // slots of raw bytes
+  static constexpr int kRawBytes = KV == 0 ? 0 : kRawData + kRawMeta;
+  static constexpr int kThreads = KV == 0 ? 384 : 512;
+  // registers: 384 x 168 or 512 x 128 at launch
+  static constexpr int kRegsSoftmax = KV == 0 ? 200 : 184, kRegsOther = KV == 0 ? 104 : 72;
+  static constexpr int kBars = 2 * kStages + 2 * kRaw + 9;
+  static constexpr int kSmem = 2 * kTile + kStages * kTile + kRaw * kRawBytes + kBars * 8 + 64 + 1024;
+};
+
+struct Unit {
+  AttendSeg sg;
+  int head, r0, n_rows;   // first packed row, rows of the session
+  int p_lo, p_hi;         // positions of the unit's first and last token
+  int key0, n_steps;      // first key (a pool block's first), steps
+};
+
+__host__ __device__ inline int unit_steps(int pos0, int n_rows, int G, int window, int r0, int& p_lo, int& p_hi,
+                                          int& key0) {
+  const int r1 = (r0 + 2 * kRows < n_rows ? r0 + 2 * kRows : n_rows) - 1;
+  p_lo = pos0 + r0 / G;
+  p_hi = pos0 + r1 / G;
+  const int first = window && p_lo - window + 1 > 0 ? p_lo - window + 1 : 0;
+  key0 = first & ~15;
+  return (p_hi - key0) / kKeys + 1;
+}
+
+// Unit u: (session, head, tile pair), the pair fastest.
+__device__ __forceinline__ Unit unit_at(const AttendArgs& a, int u) {
+  Unit x;
+  int si = 0;
+  for (int i = 1; i < a.n_seg; ++i)
+    if (u >= a.seg[i].unit0) si = i;
+  x.sg = a.seg[si];
+  const int v = u - x.sg.unit0;
+  x.head = v / x.sg.n_tiles;
+  x.r0 = (v - x.head * x.sg.n_tiles) * 2 * kRows;
+  x.n_rows = x.sg.n_tok * a.group;
+  x.n_steps = unit_steps(x.sg.pos0, x.n_rows, a.group, a.window, x.r0, x.p_lo, x.p_hi, x.key0);
+  return x;
+}
+
+// f(unit, index, first step, end step) for every piece of this block's share.
+template <typename F>
+__device__ __forceinline__ void for_share(const AttendArgs& a, const AttendShares& sh, F f) {
+  int u = sh.unit[blockIdx.x], s = sh.step[blockIdx.x];
+  const int ue = sh.unit[blockIdx.x + 1], se = sh.step[blockIdx.x + 1];
+  while (u < ue || (u == ue && s < se)) {
+    const Unit x = unit_at(a, u);
+    const int e = u == ue ? se : x.n_steps;
+    if (!f(x, u, s, e)) return;
+    ++u;
+    s = 0;
+  }
+}
+
+// 8 stored values as fp16 in order.
+template <int KV>
+__device__ __forceinline__ uint4 expand8(const uint8_t* data, uint32_t meta) {
+  uint32_t r[4];
+  if constexpr (KV == 1) {
+    const uint2 c = *reinterpret_cast<const uint2*>(data);
+    const uint32_t cw[2] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u};
+    const __half2 s = __low2half2(u32_as_h2(meta));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t h = __byte_perm(cw[i >> 1], 0x64646464u, (i & 1) ? 0x4342 : 0x4140);
+      r[i] = h2_as_u32(__hmul2(__hsub2(u32_as_h2(h), u32_as_h2(0x64806480u)), s));
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+  } else {
+    const uint32_t c = *reinterpret_cast<const uint32_t*>(data);
+    const __half2 s = __low2half2(u32_as_h2(meta)), m = __high2half2(u32_as_h2(meta));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      r[i] = h2_as_u32(
+          __hfma2(__hsub2(u32_as_h2(((c >> (4 * i)) & 0x000F000Fu) | 0x64006400u), u32_as_h2(0x64006400u)), s, m));
+    return make_uint4(__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[2], r[3], 0x5410),
+                      __byte_perm(r[0], r[1], 0x7632), __byte_perm(r[2], r[3], 0x7632));
+  }
+}
+
+template <int D, int KV>
+__global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
+    attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ AttendArgs a,
+                     const __grid_constant__ AttendShares sh) {
+  using C = Cfg<D, KV>;
+  constexpr int ST = C::kStages, RAW = C::kRaw;
+  constexpr uint32_t kIdescQK = (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+  constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* q_s = smem;                         // [2][128 rows x D]
+  uint8_t* ring = smem + 2 * C::kTile;         // [ST][128 keys x D]
+  uint8_t* raw = ring + ST * C::kTile;         // [RAW] stored bytes: data, then scales
+  uint64_t* full = reinterpret_cast<uint64_t*>(raw + RAW * C::kRawBytes);
+  uint64_t* empty = full + ST;
+  uint64_t* raw_full = empty + ST;
+  uint64_t* raw_empty = raw_full + RAW;
+  uint64_t* q_full = raw_empty + RAW;  // [2]: Q of the tile is in shared memory
+  uint64_t* s_full = q_full + 2;   // [2]: S of the tile is in tensor memory (and o holds every earlier step)
+  uint64_t* p_full = s_full + 2;   // [2]: P is
+  uint64_t* o_full = p_full + 2;   // [2]: o is final
+  uint64_t* mma_done = o_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);  // and [1], [2]: the tiles' last-arrival flags
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const PoolGeom& P = a.pool;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mb_init(full + i, KV == 0 ? 1 : 4);
+      mb_init(empty + i, 1);
+    }
+    for (int i = 0; i < RAW; ++i) {
+      mb_init(raw_full + i, 1);
+      mb_init(raw_empty + i, 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mb_init(q_full + i, 4);
+      mb_init(s_full + i, 1);
+      mb_init(p_full + i, 4);
+      mb_init(o_full + i, 1);
+    }
+    mb_init(mma_done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(tmem_slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tm_s = tmem, tm_o = tmem + 2 * kKeys;  // S (and P) of tile t at + 128 t, o of tile t at + 128 t
+
+  if (warp < 4) {
+    regs_dec<C::kRegsOther>();
+    if (warp == 0) {
+      // ---- loader: K and V of every step, in the order the MMAs use them
+      const int32_t* table = nullptr;
+      const uint8_t* layer_base = P.base + (int64_t)a.layer * P.pool_blocks * P.block_bytes;
+      const int64_t data_part = (int64_t)P.n_kv_heads * 16 * C::kRowB, meta_part = (int64_t)P.n_kv_heads * 16 * C::kMetaB;
+      int g = 0;
+      for_share(a, sh, [&](const Unit& x, int, int s0, int s1) {
+        table = P.tables + (int64_t)x.sg.sess * P.table_stride;
+        const int len = x.sg.pos0 + x.sg.n_tok, n_blk = (len + 15) >> 4;
+        int ids = 0;
+        for (int s = s0; s < s1; ++s) {
+          const int key = x.key0 + s * kKeys, b0 = key >> 4;
+          if (((s - s0) & 3) == 0) {  // the ids of four steps, one a lane
+            const int b = b0 + lane;
+            ids = b < n_blk ? checked_block(table[b], (int)P.pool_blocks, a.err) : 0;
+          }
+          const int nb = min(8, n_blk - b0);                  // pool blocks of this step
+          const int nv = min(8, (len - key) >> 4);            // of them, whole ones
+          const int my = __shfl_sync(0xffffffffu, ids, ((s - s0) & 3) * 8 + (lane & 7));
+          for (int part = 0; part < 2; ++part, ++g) {
+            if constexpr (KV == 0) {
+              const int st = g % ST;
+              if (g >= ST && !mb_wait(empty + st, ((g / ST) - 1) & 1)) {
+                if (lane == 0) atomicOr(a.err, kErrAttend);
+                return false;
+              }
+              const uint32_t dst = su32(ring + st * C::kTile);
+              int n_tma = nb;
+              if (part == 1 && nv < 8) {
+                // the step that holds the session's end: value rows past it are zeros (a slot there may hold anything,
+                // and 0 times it must be 0), the block it lies in is copied row by row
+                n_tma = nv;
+                const int y0 = nv * 16;
+                for (int i = lane; i < (kKeys - y0) * (D / 8); i += 32) {  // a multiple of 32
+                  const int row = y0 + i / (D / 8), c = i % (D / 8);
+                  uint4 w = make_uint4(0, 0, 0, 0);
+                  const int b = __shfl_sync(0xffffffffu, ids, ((s - s0) & 3) * 8 + (row >> 4));
+                  if (key + row < len)
+                    w = *reinterpret_cast<const uint4*>(layer_base + (int64_t)b * P.block_bytes + data_part +
+                                                        ((int64_t)x.head * 16 + (row & 15)) * C::kRowB + 16 * c);
+                  *reinterpret_cast<uint4*>(ring + st * C::kTile + (c >> 3) * C::kHalf + row * 128 +
+                                            (((c & 7) ^ (row & 7)) << 4)) = w;
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+              }
+              if (lane == 0) mb_expect(full + st, (uint32_t)n_tma * 16 * D * 2);
+              __syncwarp();
+              const int blk = lane & 7, half = lane >> 3;
+              if (blk < n_tma && half < D / 64)
+                tma_2d(dst + half * C::kHalf + blk * 2048, &map, half * 64,
+                       ((my * 2 + part) * P.n_kv_heads + x.head) * 16, full + st);
+            } else {
+              const int r = g % RAW;
+              if (g >= RAW && !mb_wait(raw_empty + r, ((g / RAW) - 1) & 1)) {
+                if (lane == 0) atomicOr(a.err, kErrAttend);
+                return false;
+              }
+              const uint32_t dst = su32(raw + r * C::kRawBytes);
+              if (lane == 0) mb_expect(raw_full + r, (uint32_t)nb * 16 * (C::kRowB + C::kMetaB));
+              __syncwarp();
+              const int blk = lane & 7;
+              const uint8_t* base = layer_base + (int64_t)my * P.block_bytes;
+              if (lane < nb)
+                bulk_g2s(dst + blk * 16 * C::kRowB, base + part * data_part + (int64_t)x.head * 16 * C::kRowB,
+                         16 * C::kRowB, raw_full + r);
+              else if (lane >= 8 && lane < 8 + nb)
+                bulk_g2s(dst + C::kRawData + blk * 16 * C::kMetaB,
+                         base + 2 * data_part + part * meta_part + (int64_t)x.head * 16 * C::kMetaB, 16 * C::kMetaB,
+                         raw_full + r);
+            }
+          }
+        }
+        return true;
+      });
+      // leave no copy in flight, also when a consumer gave up and will not wait for it
+      if constexpr (KV == 0) {
+        for (int f = max(0, g - ST); f < g; ++f) mb_wait(full + f % ST, (f / ST) & 1);
+      } else {
+        for (int f = max(0, g - RAW); f < g; ++f) mb_wait(raw_full + f % RAW, (f / RAW) & 1);
+      }
+    } else if (warp == 1 && lane == 0) {
+      // ---- MMA issuer
+      int g = 0, pieces[2] = {0, 0}, cnt[2] = {0, 0};
+      const uint32_t q_a = su32(q_s), ring_a = su32(ring);
+      auto qk = [&](int t, int st) {
+        const uint64_t qd = smem_desc(q_a + t * C::kTile, 16), kd = smem_desc(ring_a + st * C::kTile, 16);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t off = (uint64_t)((k >> 2) * C::kHalf + (k & 3) * 32) >> 4;
+          mma_ss(tm_s + t * kKeys, qd + off, kd + off, kIdescQK, k != 0);
+        }
+        mma_commit(s_full + t);
+      };
+      for_share(a, sh, [&](const Unit& x, int, int s0, int s1) {
+        const int nt = x.n_rows - x.r0 > kRows ? 2 : 1, n = s1 - s0;
+        bool ok = mb_wait(full + g % ST, (g / ST) & 1);
+        for (int t = 0; t < nt && ok; ++t) ok = mb_wait(q_full + t, pieces[t] & 1);
+        if (ok) {
+          tc_after();
+          for (int t = 0; t < nt; ++t) qk(t, g % ST);
+          mma_commit(empty + g % ST);
+          for (int j = 0; j < n && ok; ++j) {
+            const int gv = g + 1 + 2 * j, sv = gv % ST, sk = (gv + 1) % ST;
+            const bool next = j + 1 < n;
+            ok = mb_wait(full + sv, (gv / ST) & 1);
+            for (int t = 0; t < nt && ok; ++t) {
+              ok = mb_wait(p_full + t, (cnt[t] + j) & 1);
+              if (!ok) break;
+              tc_after();
+              const uint64_t vd = smem_desc(ring_a + sv * C::kTile, C::kHalf);
+#pragma unroll
+              for (int k = 0; k < kKeys / 16; ++k)
+                mma_ts(tm_o + t * 128, tm_s + t * kKeys + k * 8, vd + ((uint64_t)(k * 2048) >> 4), kIdescPV,
+                       (j | k) != 0);
+              if (next) {
+                if (t == 0) {
+                  ok = mb_wait(full + sk, ((gv + 1) / ST) & 1);
+                  if (!ok) break;
+                  tc_after();
+                }
+                qk(t, sk);
+              } else {
+                mma_commit(o_full + t);
+              }
+            }
+            if (!ok) break;
+            mma_commit(empty + sv);
+            if (next) mma_commit(empty + sk);
+          }
+        }
+        if (!ok) {
+          atomicOr(a.err, kErrAttend);
+          return false;
+        }
+        g += 2 * n;
+        for (int t = 0; t < nt; ++t) ++pieces[t], cnt[t] += n;
+        return true;
+      });
+      // every MMA has completed before the block frees its tensor memory
+      mma_commit(mma_done);
+      mb_wait(mma_done, 0);
+    }
+  } else if (KV != 0 && warp >= 12) {
+    // ---- expansion of INT8 / INT4 tiles, 8 values a thread at a time
+    regs_dec<C::kRegsOther>();
+    if constexpr (KV != 0) {
+      const int w = warp - 12;
+      int g = 0;
+      for_share(a, sh, [&](const Unit& x, int, int s0, int s1) {
+        const int len = x.sg.pos0 + x.sg.n_tok;
+        for (int s = s0; s < s1; ++s) {
+          const int live = len - (x.key0 + s * kKeys);  // rows that hold tokens
+          for (int part = 0; part < 2; ++part, ++g) {
+            const int r = g % RAW, st = g % ST;
+            if (!mb_wait(raw_full + r, (g / RAW) & 1) || (g >= ST && !mb_wait(empty + st, ((g / ST) - 1) & 1))) {
+              if (lane == 0) atomicOr(a.err, kErrAttend);
+              return false;
+            }
+            const uint8_t* src = raw + r * C::kRawBytes;
+            uint8_t* dst = ring + st * C::kTile;
+#pragma unroll 4
+            for (int i = 0; i < kKeys * D / 8 / 128; ++i) {
+              // 8 lanes a 128-byte row of a half, 4 rows a warp
+              const int item = i * 16 + w * 4 + (lane >> 3);
+              const int row = item % kKeys, c = (item / kKeys) * 8 + (lane & 7);
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (row < live) {
+                const uint8_t* mp = src + C::kRawData + row * C::kMetaB;
+                const uint32_t meta = KV == 1 ? *reinterpret_cast<const uint16_t*>(mp)
+                                              : reinterpret_cast<const uint32_t*>(mp)[c >> 2];
+                v = expand8<KV>(src + row * C::kRowB + c * (KV == 1 ? 8 : 4), meta);
+              }
+              *reinterpret_cast<uint4*>(dst + (c >> 3) * C::kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+              mb_arrive(raw_empty + r);
+              mb_arrive(full + st);
+            }
+          }
+        }
+        return true;
+      });
+    }
+  } else {
+    // ---- softmax of row tile t, one row a thread
+    regs_inc<C::kRegsSoftmax>();
+    const int t = (warp >> 2) - 1, row = threadIdx.x & 127;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tm_s + t * kKeys + lane_base, to = tm_o + t * 128 + lane_base;
+    const float scale = fabsf(a.scale_log2) > 0.f ? fabsf(a.scale_log2) : 1.f;
+    const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale: -q with its absolute value
+    const bool zero = a.scale_log2 == 0.f;                        // every score 0
+    const int G = a.group;
+    int cnt = 0, n_o = 0;
+    for_share(a, sh, [&](const Unit& x, int u, int s0, int s1) {
+      // Q of the tile into its swizzled place (every MMA that read the previous one is done)
+      if (x.n_rows - x.r0 <= t * kRows) return true;  // no such tile
+      {
+        uint8_t* qt = q_s + t * C::kTile;
+        constexpr int cpr = D / 8;  // 16-byte runs of a row
+#pragma unroll 8
+        for (int i = threadIdx.x & 127; i < kRows * cpr; i += 128) {
+          const int rr = i / cpr, c = i % cpr, r = x.r0 + t * kRows + rr;
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (r < x.n_rows && !zero)
+            w = ldg_stream_u4(a.q + (int64_t)(x.sg.row0 + r / G) * a.ldq + (int64_t)(x.head * G + r % G) * D + 8 * c);
+          w.x ^= flip, w.y ^= flip, w.z ^= flip, w.w ^= flip;
+          *reinterpret_cast<uint4*>(qt + (c >> 3) * C::kHalf + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = w;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      __syncwarp();
+      if (lane == 0) mb_arrive(q_full + t);
+
+      const int r = x.r0 + t * kRows + row;
+      const int pos = x.sg.pos0 + min(r, x.n_rows - 1) / G;
+      // positions of the tile's first and last token: which steps need a mask
+      const int t_lo = x.sg.pos0 + (x.r0 + t * kRows) / G;
+      const int t_hi = x.sg.pos0 + (min(x.r0 + t * kRows + kRows, x.n_rows) - 1) / G;
+      float m = -INFINITY, l = 0.f;
+      for (int s = s0; s < s1; ++s, ++cnt) {
+        if (!mb_wait(s_full + t, cnt & 1)) {
+          if (lane == 0) atomicOr(a.err, kErrAttend);
+          return false;
+        }
+        tc_after();
+        float v[kKeys];
+#pragma unroll
+        for (int c = 0; c < kKeys; c += 32) tmem_ld32(ts + c, v + c);
+        tmem_wait_ld();
+        const int key = x.key0 + s * kKeys;
+        if (key + kKeys - 1 > t_lo || (a.window && key <= t_hi - a.window)) {
+          const int hi = pos - key, lo = a.window ? hi - a.window + 1 : -1;  // columns lo .. hi are seen
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c)
+            if (c > hi || c < lo) v[c] = -INFINITY;
+        }
+        float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int c = 4; c + 8 <= kKeys; c += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], v[c + i], v[c + 4 + i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], v[kKeys - 4 + i]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+        const bool raise = top > m + kLazy;
+        if (__any_sync(0xffffffffu, raise)) {
+          const float mn = fmaxf(m, top);
+          const float f = m == -INFINITY ? 0.f : ex2(m - mn);
+          m = mn;
+          l *= f;
+          if (s > s0) {
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+              float o[32];
+              tmem_ld32(to + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= f;
+              tmem_st32(to + c, o);
+            }
+          }
+        }
+        const float off = kShift - (m == -INFINITY ? 0.f : m);
+        const F2 sc2 = f2(scale, scale), off2 = f2(off, off);
+        F2 sum[2] = {f2(l, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < kKeys; c += 32) {
+          uint32_t p[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float e0, e1;
+            unpack(fma2(f2(v[c + 2 * i], v[c + 2 * i + 1]), sc2, off2), e0, e1);
+            e0 = ex2(e0), e1 = ex2(e1);
+            sum[i & 1] = add2(sum[i & 1], f2(e0, e1));
+            p[i] = h2_as_u32(__floats2half2_rn(e0, e1));
+          }
+          tmem_st16(ts + c / 2, p);
+        }
+        float a0, a1, b0, b1;
+        unpack(sum[0], a0, a1);
+        unpack(sum[1], b0, b1);
+        l = (a0 + a1) + (b0 + b1);
+        tmem_wait_st();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mb_arrive(p_full + t);
+      }
+      // ---- the piece's result
+      if (!mb_wait(o_full + t, n_o & 1)) {
+        if (lane == 0) atomicOr(a.err, kErrAttend);
+        return false;
+      }
+      ++n_o;
+      tc_after();
+      const bool live = r < x.n_rows;
+      __half* dst = a.o + (int64_t)(x.sg.row0 + r / G) * a.ldo + (int64_t)(x.head * G + r % G) * D;
+      auto store = [&](int c, const float* o, float inv) {
+        if (!live) return;
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+          uint4 w;
+          w.x = h2_as_u32(__floats2half2_rn(o[i] * inv, o[i + 1] * inv));
+          w.y = h2_as_u32(__floats2half2_rn(o[i + 2] * inv, o[i + 3] * inv));
+          w.z = h2_as_u32(__floats2half2_rn(o[i + 4] * inv, o[i + 5] * inv));
+          w.w = h2_as_u32(__floats2half2_rn(o[i + 6] * inv, o[i + 7] * inv));
+          *reinterpret_cast<uint4*>(dst + c + i) = w;
+        }
+      };
+      if (s0 == 0 && s1 == x.n_steps) {
+        const float inv = 1.0f / l;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(to + c, o);
+          tmem_wait_ld();
+          store(c, o, inv);
+        }
+        return true;
+      }
+      // a cut unit: this block's part, column by column ([2 per block][tile][D + 2][128])
+      constexpr int kPart = (D + 2) * kRows;
+      const int mine = 2 * (int)blockIdx.x + (u == sh.unit[blockIdx.x] ? 0 : 1);
+      float* part = a.part + (int64_t)(2 * mine + t) * kPart + row;
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        tmem_ld32(to + c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) __stcg(part + (c + i) * kRows, o[i]);
+      }
+      __stcg(part + D * kRows, m);
+      __stcg(part + (D + 1) * kRows, l);
+      __threadfence();
+      // the blocks that share the unit: from the one where it begins
+      int b0 = blockIdx.x, b1 = blockIdx.x;
+      while (sh.unit[b0] == u && sh.step[b0] > 0) --b0;
+      while (sh.unit[b1 + 1] == u && sh.step[b1 + 1] < x.n_steps) ++b1;
+      wg_sync(1 + t);
+      if (row == 0) {
+        uint32_t* cnt_p = a.arrivals + 2 * b0 + t;
+        const uint32_t prev = atomicAdd(cnt_p, 1u);
+        const bool last = (int)prev == b1 - b0;
+        if (last) *cnt_p = 0;  // for the next launch
+        tmem_slot[1 + t] = last;
+      }
+      wg_sync(1 + t);
+      if (!tmem_slot[1 + t]) return true;
+      __threadfence();
+      auto part_of = [&](int b) {
+        const int slot = 2 * b + (u == sh.unit[b] ? 0 : 1);
+        return a.part + (int64_t)(2 * slot + t) * kPart + row;
+      };
+      float mt = -INFINITY, lt = 0.f;
+      for (int b = b0; b <= b1; ++b) mt = fmaxf(mt, __ldcg(part_of(b) + D * kRows));
+      for (int b = b0; b <= b1; ++b) {
+        const float mb = __ldcg(part_of(b) + D * kRows);
+        lt = fmaf(mb == -INFINITY ? 0.f : ex2(mb - mt), __ldcg(part_of(b) + (D + 1) * kRows), lt);
+      }
+      const float inv = 1.0f / lt;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = 0.f;
+        for (int b = b0; b <= b1; ++b) {
+          const float* pb = part_of(b);
+          const float mb = __ldcg(pb + D * kRows);
+          const float f = mb == -INFINITY ? 0.f : ex2(mb - mt);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = fmaf(f, __ldcg(pb + (c + i) * kRows), o[i]);
+        }
+        store(c, o, inv);
+      }
+      return true;
+    });
+  }
+  tc_before();
+  __syncthreads();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = [] {
+    cudaDriverEntryPointQueryResult q;
+    void* p = nullptr;
+    return cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<EncodeTiledFn>(p)
+               : nullptr;
+  }();
+  return fn;
+}
+
+template <int D, int KV>
+cudaError_t launch_tc_t(const Launch& L, const AttendArgs& a, const AttendShares& sh) {
+  using C = Cfg<D, KV>;
+  static_assert(C::kSmem <= 227 * 1024, "shared memory");
+  alignas(64) CUtensorMap map = {};
+  if (KV == 0) {  // the layer's pool blocks as rows of D values: [block][K, V][head][16]
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return cudaErrorNotSupported;
+    cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)a.pool.pool_blocks * 2 * a.pool.n_kv_heads * 16};
+    cuuint64_t strides[1] = {(cuuint64_t)D * 2};
+    cuuint32_t box[2] = {64, 16}, es[2] = {1, 1};
+    void* base = a.pool.base + (int64_t)a.layer * a.pool.pool_blocks * a.pool.block_bytes;
+    if (fn(&map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  cudaError_t e = cudaFuncSetAttribute(attend_tc_kernel<D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  attend_tc_kernel<D, KV><<<sh.n, C::kThreads, C::kSmem, L.stream>>>(map, a, sh);
+  if (L.counter) ++*L.counter;
+  return cudaGetLastError();
+}
+template <int D>
+cudaError_t launch_tc_kv(const Launch& L, const AttendArgs& a, const AttendShares& sh) {
+  switch (a.pool.kv_dtype) {
+    case 0: return launch_tc_t<D, 0>(L, a, sh);
+    case 1: return launch_tc_t<D, 1>(L, a, sh);
+    default: return launch_tc_t<D, 2>(L, a, sh);
+  }
+}
+
+}  // namespace
+
+bool attend_tc_shares(AttendArgs& a, int n_sm, AttendShares& sh) {
+  // rows of the tensor map are 32-bit signed coordinates
+  if (a.pool.pool_blocks * 2 * a.pool.n_kv_heads * 16 >= (int64_t)1 << 31) return false;
+  int64_t total = 0, units = 0;
+  int p_lo, p_hi, key0;
+  auto seg_steps = [&](const AttendSeg& s) {  // steps of all tile pairs of one head
+    const int rows = s.n_tok * a.group;
+    int64_t n = 0;
+    for (int i = 0; i < s.n_tiles; ++i) n += unit_steps(s.pos0, rows, a.group, a.window, i * 2 * kRows, p_lo, p_hi, key0);
+    return n;
+  };
+  int64_t per_head[MAG_MAX_BATCH];
+  for (int i = 0; i < a.n_seg; ++i) {
+    AttendSeg& s = a.seg[i];
+    s.n_tiles = (s.n_tok * a.group + 2 * kRows - 1) / (2 * kRows);
+    s.unit0 = (int32_t)units;
+    units += (int64_t)s.n_tiles * a.n_kv_heads;
+    per_head[i] = seg_steps(s);
+    total += per_head[i] * a.n_kv_heads;
+  }
+  a.n_units = (int32_t)units;
+  // every block at least two steps: a merge costs about as much
+  sh.n = (int32_t)std::max<int64_t>(1, std::min<int64_t>(std::min(n_sm, kAttendMaxShares), (total + 1) / 2));
+  // the share boundaries: block b begins at step floor(total b / n) of all units in order
+  int si = 0, head = 0, tile = 0;
+  int64_t at = 0;
+  for (int b = 0; b < sh.n; ++b) {
+    const int64_t want = total * b / sh.n;
+    while (true) {
+      const AttendSeg& s = a.seg[si];
+      if (tile == 0 && at + per_head[si] <= want) {  // a whole head further
+        at += per_head[si];
+        if (++head == a.n_kv_heads) head = 0, ++si;
+        continue;
+      }
+      const int n = unit_steps(s.pos0, s.n_tok * a.group, a.group, a.window, tile * 2 * kRows, p_lo, p_hi, key0);
+      if (at + n > want) break;
+      at += n;
+      if (++tile == s.n_tiles) {
+        tile = 0;
+        if (++head == a.n_kv_heads) head = 0, ++si;
+      }
+    }
+    sh.unit[b] = a.seg[si].unit0 + head * a.seg[si].n_tiles + tile;
+    sh.step[b] = (int32_t)(want - at);
+  }
+  sh.unit[sh.n] = a.n_units;
+  sh.step[sh.n] = 0;
+  return true;
+}
+
+cudaError_t launch_attend_tc(const Launch& L, const AttendArgs& a, const AttendShares& sh) {
+  if (a.n_units < 1 || a.n_seg < 1 || a.n_seg > MAG_MAX_BATCH || sh.n < 1 || sh.n > kAttendMaxShares)
+    return cudaErrorInvalidValue;
+  return a.pool.head_dim == 64 ? launch_tc_kv<64>(L, a, sh) : launch_tc_kv<128>(L, a, sh);
+}
+
+}  // namespace mag

@@ -305,6 +305,16 @@ struct AttendArgs {
 constexpr int kAttendMaxSplitBlocks = 2048;  // blocks of one launch that may leave partial results
 constexpr size_t kAttendPartRows = (size_t)kAttendMaxSplitBlocks * 16, kAttendPartFloats = kAttendPartRows * 128;
 cudaError_t launch_attend_few(const Launch& L, const AttendArgs& a, int tile_rows);
+// Many rows (tcgen05): block b takes the steps from (unit[b], step[b]) up to (unit[b + 1], step[b + 1]).
+constexpr int kAttendMaxShares = 160;
+struct AttendShares {
+  int32_t n;
+  int32_t unit[kAttendMaxShares + 1], step[kAttendMaxShares + 1];
+};
+constexpr size_t kAttendSharePartFloats = (size_t)kAttendMaxShares * 4 * 130 * 128;  // two cut pieces of two tiles a block
+// Fills the sessions' units and the shares from n_seg and the sessions' rows; false where the kernel cannot run.
+bool attend_tc_shares(AttendArgs& a, int n_sm, AttendShares& sh);
+cudaError_t launch_attend_tc(const Launch& L, const AttendArgs& a, const AttendShares& sh);
 
 // ---------------------------------------------------------------- sampling
 struct SampleArgs {

@@ -63,7 +63,7 @@ static int read_blocks(const KvRows& r, int32_t* blk0) {
 // The workspace of split attention tiles, made by the first call that needs it.
 static mag_status attend_workspace(mag_ctx* c) {
   if (c->at_part) return MAG_OK;
-  const size_t part = kAttendPartFloats * 4, ml = kAttendPartRows * 2 * 4, cnt = (size_t)kAttendMaxSplitBlocks * 4;
+  const size_t part = std::max(kAttendPartFloats, kAttendSharePartFloats) * 4, ml = kAttendPartRows * 2 * 4, cnt = (size_t)kAttendMaxSplitBlocks * 4;
   cudaError_t e;
   float *p = nullptr, *m = nullptr;
   uint32_t* n = nullptr;
@@ -120,7 +120,9 @@ static void attend_units(const mag_ctx* c, AttendArgs& a, const KvRows& rows, in
   a.n_units = (int32_t)unit;
 }
 
-mag_status run_attend(mag_ctx* c, int32_t layer, const KvRows& rows, const void* q, int64_t ldq, void* out, int64_t ldo,
+constexpr int kFewRows = 16;  // most packed rows of a session for the few-row kernel
+
+static mag_status run_attend(mag_ctx* c, int32_t layer, const KvRows& rows, const void* q, int64_t ldq, void* out, int64_t ldo,
                       int32_t window, float scale) {
   AttendArgs a = {};
   a.q = (const __half*)q;
@@ -135,20 +137,48 @@ mag_status run_attend(mag_ctx* c, int32_t layer, const KvRows& rows, const void*
   a.scale_log2 = scale * 1.44269504088896340736f;
   a.pool = pool_geom(c);
   a.err = c->d_err;
-  int most = 0;
-  for (int i = 0; i < rows.n_seg; ++i) most = std::max(most, rows.seg[i].n_tok);
-  const int tile_rows = (int64_t)most * c->G <= 8 ? 8 : 16;
-  attend_units(c, a, rows, tile_rows, std::min(4 * c->n_sm, kAttendMaxSplitBlocks / 2), 8);
-  bool split = false;
-  for (int i = 0; i < a.n_seg; ++i) split |= a.seg[i].n_split > 1;
-  if (split) {
-    const mag_status st = attend_workspace(c);
-    if (st != MAG_OK) return st;
+  // Sessions of up to 16 packed rows go to the few-row kernel, the others to the tensor-core one
+  const Launch L{c->stream, false, nullptr};
+  for (int many = 0; many < 2; ++many) {
+    KvRows part = {};
+    int most = 0;
+    for (int i = 0; i < rows.n_seg; ++i) {
+      const int64_t n = (int64_t)rows.seg[i].n_tok * c->G;
+      if ((n > kFewRows) != (many != 0)) continue;
+      part.seg[part.n_seg++] = rows.seg[i];
+      most = std::max(most, (int)n);
+    }
+    if (!part.n_seg) continue;
+    if (many) {
+      const mag_status st = attend_workspace(c);
+      if (st != MAG_OK) return st;
+      a.part = c->at_part;
+      a.part_ml = c->at_ml;
+      a.arrivals = c->at_arrivals;
+      a.n_seg = part.n_seg;
+      for (int i = 0; i < part.n_seg; ++i) {
+        const KvSeg& s = part.seg[i];
+        a.seg[i] = AttendSeg{s.row0, s.n_tok, s.pos0, s.sess, 0, 1, 0, 0, 0};
+      }
+      AttendShares sh;
+      if (attend_tc_shares(a, c->n_sm, sh)) {
+        CUDA_TRY(c, launch_attend_tc(L, a, sh));
+        continue;
+      }
+    }
+    const int tile_rows = most <= 8 ? 8 : 16;
+    attend_units(c, a, part, tile_rows, std::min(4 * c->n_sm, kAttendMaxSplitBlocks / 2), 8);
+    bool split = false;
+    for (int i = 0; i < a.n_seg; ++i) split |= a.seg[i].n_split > 1;
+    if (split) {
+      const mag_status st = attend_workspace(c);
+      if (st != MAG_OK) return st;
+    }
+    a.part = c->at_part;
+    a.part_ml = c->at_ml;
+    a.arrivals = c->at_arrivals;
+    CUDA_TRY(c, launch_attend_few(L, a, tile_rows));
   }
-  a.part = c->at_part;
-  a.part_ml = c->at_ml;
-  a.arrivals = c->at_arrivals;
-  CUDA_TRY(c, launch_attend_few(Launch{c->stream, false, nullptr}, a, tile_rows));
   return MAG_OK;
 }
 
