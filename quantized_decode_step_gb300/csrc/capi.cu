@@ -48,7 +48,7 @@ mag_status check_err(mag_ctx* c) {
   }
   cudaMemsetAsync(c->d_counters, 0, c->n_counters * 4, c->stream);
   cudaMemsetAsync(c->attn_arrivals, 0, (size_t)c->B_max * c->Hkv * 4, c->stream);
-  if (c->at_arrivals) cudaMemsetAsync(c->at_arrivals, 0, (size_t)kAttendMaxSplitBlocks * 4, c->stream);
+  if (c->at_arrivals) cudaMemsetAsync(c->at_arrivals, 0, kAttendArrivals * 4, c->stream);
   if (c->pf_part_cnt) cudaMemsetAsync(c->pf_part_cnt, 0, (size_t)(c->n_sm / 2) * 4 * 4, c->stream);
   return fail(c, MAG_ERR_TIMEOUT, "a kernel's pipeline wait gave up (code 0x%x)", e);
 }

@@ -201,16 +201,6 @@ struct Unit {
   int key0, n_steps;      // first key (a pool block's first), steps
 };
 
-__host__ __device__ inline int unit_steps(int pos0, int n_rows, int G, int window, int r0, int& p_lo, int& p_hi,
-                                          int& key0) {
-  const int r1 = (r0 + 2 * kRows < n_rows ? r0 + 2 * kRows : n_rows) - 1;
-  p_lo = pos0 + r0 / G;
-  p_hi = pos0 + r1 / G;
-  const int first = window && p_lo - window + 1 > 0 ? p_lo - window + 1 : 0;
-  key0 = first & ~15;
-  return (p_hi - key0) / kKeys + 1;
-}
-
 // Unit u: (session, head, tile pair), the pair fastest.
 __device__ __forceinline__ Unit unit_at(const AttendArgs& a, int u) {
   Unit x;
@@ -222,7 +212,7 @@ __device__ __forceinline__ Unit unit_at(const AttendArgs& a, int u) {
   x.head = v / x.sg.n_tiles;
   x.r0 = (v - x.head * x.sg.n_tiles) * 2 * kRows;
   x.n_rows = x.sg.n_tok * a.group;
-  x.n_steps = unit_steps(x.sg.pos0, x.n_rows, a.group, a.window, x.r0, x.p_lo, x.p_hi, x.key0);
+  x.n_steps = attend_unit_steps(x.sg.pos0, x.n_rows, a.group, a.window, x.r0, 2 * kRows, kKeys, x.p_lo, x.p_hi, x.key0);
   return x;
 }
 
@@ -757,60 +747,16 @@ cudaError_t launch_tc_kv(const Launch& L, const AttendArgs& a, const AttendShare
 
 }  // namespace
 
-bool attend_tc_shares(AttendArgs& a, int n_sm, AttendShares& sh) {
+bool attend_tc_fits(const AttendArgs& a) {
   // rows of the tensor map are 32-bit signed coordinates
-  if (a.pool.pool_blocks * 2 * a.pool.n_kv_heads * 16 >= (int64_t)1 << 31) return false;
-  int64_t total = 0, units = 0;
-  int p_lo, p_hi, key0;
-  auto seg_steps = [&](const AttendSeg& s) {  // steps of all tile pairs of one head
-    const int rows = s.n_tok * a.group;
-    int64_t n = 0;
-    for (int i = 0; i < s.n_tiles; ++i) n += unit_steps(s.pos0, rows, a.group, a.window, i * 2 * kRows, p_lo, p_hi, key0);
-    return n;
-  };
-  int64_t per_head[MAG_MAX_BATCH];
-  for (int i = 0; i < a.n_seg; ++i) {
-    AttendSeg& s = a.seg[i];
-    s.n_tiles = (s.n_tok * a.group + 2 * kRows - 1) / (2 * kRows);
-    s.unit0 = (int32_t)units;
-    units += (int64_t)s.n_tiles * a.n_kv_heads;
-    per_head[i] = seg_steps(s);
-    total += per_head[i] * a.n_kv_heads;
-  }
-  a.n_units = (int32_t)units;
-  // every block at least two steps: a merge costs about as much
-  sh.n = (int32_t)std::max<int64_t>(1, std::min<int64_t>(std::min(n_sm, kAttendMaxShares), (total + 1) / 2));
-  // the share boundaries: block b begins at step floor(total b / n) of all units in order
-  int si = 0, head = 0, tile = 0;
-  int64_t at = 0;
-  for (int b = 0; b < sh.n; ++b) {
-    const int64_t want = total * b / sh.n;
-    while (true) {
-      const AttendSeg& s = a.seg[si];
-      if (tile == 0 && at + per_head[si] <= want) {  // a whole head further
-        at += per_head[si];
-        if (++head == a.n_kv_heads) head = 0, ++si;
-        continue;
-      }
-      const int n = unit_steps(s.pos0, s.n_tok * a.group, a.group, a.window, tile * 2 * kRows, p_lo, p_hi, key0);
-      if (at + n > want) break;
-      at += n;
-      if (++tile == s.n_tiles) {
-        tile = 0;
-        if (++head == a.n_kv_heads) head = 0, ++si;
-      }
-    }
-    sh.unit[b] = a.seg[si].unit0 + head * a.seg[si].n_tiles + tile;
-    sh.step[b] = (int32_t)(want - at);
-  }
-  sh.unit[sh.n] = a.n_units;
-  sh.step[sh.n] = 0;
-  return true;
+  return a.pool.pool_blocks * 2 * a.pool.n_kv_heads * 16 < (int64_t)1 << 31;
 }
 
-cudaError_t launch_attend_tc(const Launch& L, const AttendArgs& a, const AttendShares& sh) {
-  if (a.n_units < 1 || a.n_seg < 1 || a.n_seg > MAG_MAX_BATCH || sh.n < 1 || sh.n > kAttendMaxShares)
-    return cudaErrorInvalidValue;
+cudaError_t launch_attend_tc(const Launch& L, AttendArgs& a, int n_sm) {
+  if (a.n_seg < 1 || a.n_seg > MAG_MAX_BATCH) return cudaErrorInvalidValue;
+  // every block at least two steps: a merge costs about as much
+  AttendShares sh;
+  attend_shares(a, 2 * kRows, kKeys, n_sm, 2, sh);
   return a.pool.head_dim == 64 ? launch_tc_kv<64>(L, a, sh) : launch_tc_kv<128>(L, a, sh);
 }
 

@@ -277,13 +277,12 @@ struct KvReadArgs {
 cudaError_t launch_kv_read(const Launch& L, const KvReadArgs& a, int n_layers);
 
 // Causal grouped-query attention of the sessions' newest tokens over the pool. The G query heads of a KV head and
-// the tokens of a session are packed into rows, row t G + g, cut into tiles; a tile's keys may be split over
-// several blocks, which leave (m, l, o) in the workspace for the last of them to merge.
+// the tokens of a session are packed into rows, row t G + g, cut into tiles; a unit is one (session, KV head, tile)
+// over its keys in steps. The units' steps, in order, are dealt out to the blocks in equal shares; blocks that
+// share a unit leave (m, l, o) in the workspace for the last of them to merge.
 struct AttendSeg {
   int32_t row0, n_tok, pos0, sess;  // as KvSeg
-  int32_t unit0;                    // first block of this session
-  int32_t n_split, n_tiles;         // blocks: ((tile * Hkv) + head) * n_split + split
-  int32_t slot0, part0;             // split: first (tile, head) in the workspace's counters, first block in its parts
+  int32_t unit0, n_tiles;           // units of this session: unit0 + head * n_tiles + tile
 };
 struct AttendArgs {
   const __half* q;  // token row r, head h at q + r ldq + h d
@@ -291,30 +290,43 @@ struct AttendArgs {
   __half* o;
   int64_t ldo;
   int32_t n_heads, n_kv_heads, group, layer;
-  int32_t window;   // 0: every key up to the token's own
-  float scale_log2; // scale * log2(e)
-  float* part;      // split tiles: per block [tile rows][d] of o, fp32
-  float* part_ml;   // per block [tile rows][2]: running maximum (log2 units) and sum
-  uint32_t* arrivals;  // per (tile, head), zero between launches
+  int32_t window;      // 0: every key up to the token's own
+  float scale_log2;    // scale * log2(e)
+  float* part;         // o of cut pieces, two a block, fp32
+  float* part_ml;      // few rows: their running maxima (log2 units) and sums
+  uint32_t* arrivals;  // zero between launches
   int32_t n_seg, n_units;
   AttendSeg seg[MAG_MAX_BATCH];
   PoolGeom pool;
   uint32_t* err;
 };
-// Few rows: tiles of 8 or 16 rows.
-constexpr int kAttendMaxSplitBlocks = 2048;  // blocks of one launch that may leave partial results
-constexpr size_t kAttendPartRows = (size_t)kAttendMaxSplitBlocks * 16, kAttendPartFloats = kAttendPartRows * 128;
-cudaError_t launch_attend_few(const Launch& L, const AttendArgs& a, int tile_rows);
-// Many rows (tcgen05): block b takes the steps from (unit[b], step[b]) up to (unit[b + 1], step[b + 1]).
+// Block b takes the steps from (unit[b], step[b]) up to (unit[b + 1], step[b + 1]); no share is empty.
 constexpr int kAttendMaxShares = 160;
 struct AttendShares {
   int32_t n;
   int32_t unit[kAttendMaxShares + 1], step[kAttendMaxShares + 1];
 };
-constexpr size_t kAttendSharePartFloats = (size_t)kAttendMaxShares * 4 * 130 * 128;  // two cut pieces of two tiles a block
-// Fills the sessions' units and the shares from n_seg and the sessions' rows; false where the kernel cannot run.
-bool attend_tc_shares(AttendArgs& a, int n_sm, AttendShares& sh);
-cudaError_t launch_attend_tc(const Launch& L, const AttendArgs& a, const AttendShares& sh);
+// Steps of `step_keys` keys of the unit of rows r0 .. r0 + tile_rows - 1: from the pool block that holds the first
+// key its first token sees to its last token's own. Positions of those tokens, and the first key.
+__host__ __device__ inline int attend_unit_steps(int pos0, int n_rows, int G, int window, int r0, int tile_rows,
+                                                 int step_keys, int& p_lo, int& p_hi, int& key0) {
+  const int r1 = (r0 + tile_rows < n_rows ? r0 + tile_rows : n_rows) - 1;
+  p_lo = pos0 + r0 / G;
+  p_hi = pos0 + r1 / G;
+  const int first = window && p_lo - window + 1 > 0 ? p_lo - window + 1 : 0;
+  key0 = first & ~15;
+  return (p_hi - key0) / step_keys + 1;
+}
+void attend_shares(AttendArgs& a, int tile_rows, int step_keys, int max_blocks, int min_steps, AttendShares& sh);
+// Workspace: two cut pieces a block, of 16 rows of 128 values, or of two tiles of 128 rows of 128 values and (m, l).
+constexpr size_t kAttendPartFloats = (size_t)kAttendMaxShares * 2 * 2 * 130 * 128;
+constexpr size_t kAttendMlFloats = (size_t)kAttendMaxShares * 2 * 16 * 2;
+constexpr size_t kAttendArrivals = 2 * kAttendMaxShares;
+// Few rows: tiles of 8 or 16 rows.
+cudaError_t launch_attend_few(const Launch& L, AttendArgs& a, int n_sm, int tile_rows);
+// Many rows (tcgen05); false where the pool is too large for it.
+bool attend_tc_fits(const AttendArgs& a);
+cudaError_t launch_attend_tc(const Launch& L, AttendArgs& a, int n_sm);
 
 // ---------------------------------------------------------------- sampling
 struct SampleArgs {

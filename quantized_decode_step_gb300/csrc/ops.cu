@@ -63,7 +63,7 @@ static int read_blocks(const KvRows& r, int32_t* blk0) {
 // The workspace of split attention tiles, made by the first call that needs it.
 static mag_status attend_workspace(mag_ctx* c) {
   if (c->at_part) return MAG_OK;
-  const size_t part = std::max(kAttendPartFloats, kAttendSharePartFloats) * 4, ml = kAttendPartRows * 2 * 4, cnt = (size_t)kAttendMaxSplitBlocks * 4;
+  const size_t part = kAttendPartFloats * 4, ml = kAttendMlFloats * 4, cnt = kAttendArrivals * 4;
   cudaError_t e;
   float *p = nullptr, *m = nullptr;
   uint32_t* n = nullptr;
@@ -86,40 +86,6 @@ static mag_status attend_workspace(mag_ctx* c) {
   return MAG_OK;
 }
 
-// The sessions of a launch cut into blocks: tiles of tile_rows packed rows, each tile's keys in n_split parts so
-// that about `target` blocks come out, of no fewer than min_blocks pool blocks each.
-static void attend_units(const mag_ctx* c, AttendArgs& a, const KvRows& rows, int tile_rows, int64_t target,
-                         int min_blocks) {
-  int64_t work = 0;  // pool blocks over all tiles, with every tile at its session's length
-  for (int i = 0; i < rows.n_seg; ++i) {
-    const KvSeg& s = rows.seg[i];
-    const int64_t tiles = ((int64_t)s.n_tok * c->G + tile_rows - 1) / tile_rows;
-    int64_t keys = s.pos0 + s.n_tok;
-    if (a.window) keys = std::min<int64_t>(keys, a.window + (tile_rows + c->G - 1) / c->G);
-    work += tiles * c->Hkv * ((keys + 15) / 16);
-  }
-  const int64_t per = std::max<int64_t>(min_blocks, (work + target - 1) / target);
-  int64_t unit = 0, slot = 0, part = 0;
-  a.n_seg = rows.n_seg;
-  for (int i = 0; i < rows.n_seg; ++i) {
-    const KvSeg& s = rows.seg[i];
-    const int tiles = (int)(((int64_t)s.n_tok * c->G + tile_rows - 1) / tile_rows);
-    int64_t keys = s.pos0 + s.n_tok;
-    if (a.window) keys = std::min<int64_t>(keys, a.window + (tile_rows + c->G - 1) / c->G);
-    int split = (int)(((keys + 15) / 16 + per - 1) / per);
-    // a split tile has more than `per` blocks, so there are fewer than `target` of them and fewer than
-    // 2 target parts; whatever the arithmetic, no more than the workspace holds
-    if (split > 1 && part + (int64_t)tiles * c->Hkv * split > kAttendMaxSplitBlocks) split = 1;
-    a.seg[i] = AttendSeg{s.row0, s.n_tok, s.pos0, s.sess, (int32_t)unit, split, tiles, (int32_t)slot, (int32_t)part};
-    unit += (int64_t)tiles * c->Hkv * split;
-    if (split > 1) {
-      slot += (int64_t)tiles * c->Hkv;
-      part += (int64_t)tiles * c->Hkv * split;
-    }
-  }
-  a.n_units = (int32_t)unit;
-}
-
 constexpr int kFewRows = 16;  // most packed rows of a session for the few-row kernel
 
 static mag_status run_attend(mag_ctx* c, int32_t layer, const KvRows& rows, const void* q, int64_t ldq, void* out, int64_t ldo,
@@ -137,47 +103,26 @@ static mag_status run_attend(mag_ctx* c, int32_t layer, const KvRows& rows, cons
   a.scale_log2 = scale * 1.44269504088896340736f;
   a.pool = pool_geom(c);
   a.err = c->d_err;
-  // Sessions of up to 16 packed rows go to the few-row kernel, the others to the tensor-core one
+  const mag_status ws = attend_workspace(c);
+  if (ws != MAG_OK) return ws;
+  a.part = c->at_part;
+  a.part_ml = c->at_ml;
+  a.arrivals = c->at_arrivals;
   const Launch L{c->stream, false, nullptr};
+  const bool tc = attend_tc_fits(a);
+  // sessions of up to kFewRows packed rows, then the others
   for (int many = 0; many < 2; ++many) {
-    KvRows part = {};
-    int most = 0;
+    int64_t most = 0;
+    a.n_seg = 0;
     for (int i = 0; i < rows.n_seg; ++i) {
-      const int64_t n = (int64_t)rows.seg[i].n_tok * c->G;
-      if ((n > kFewRows) != (many != 0)) continue;
-      part.seg[part.n_seg++] = rows.seg[i];
-      most = std::max(most, (int)n);
+      const KvSeg& s = rows.seg[i];
+      const int64_t n = (int64_t)s.n_tok * c->G;
+      if ((tc && n > kFewRows) != (many != 0)) continue;
+      a.seg[a.n_seg++] = AttendSeg{s.row0, s.n_tok, s.pos0, s.sess, 0, 0};
+      most = std::max(most, n);
     }
-    if (!part.n_seg) continue;
-    if (many) {
-      const mag_status st = attend_workspace(c);
-      if (st != MAG_OK) return st;
-      a.part = c->at_part;
-      a.part_ml = c->at_ml;
-      a.arrivals = c->at_arrivals;
-      a.n_seg = part.n_seg;
-      for (int i = 0; i < part.n_seg; ++i) {
-        const KvSeg& s = part.seg[i];
-        a.seg[i] = AttendSeg{s.row0, s.n_tok, s.pos0, s.sess, 0, 1, 0, 0, 0};
-      }
-      AttendShares sh;
-      if (attend_tc_shares(a, c->n_sm, sh)) {
-        CUDA_TRY(c, launch_attend_tc(L, a, sh));
-        continue;
-      }
-    }
-    const int tile_rows = most <= 8 ? 8 : 16;
-    attend_units(c, a, part, tile_rows, std::min(4 * c->n_sm, kAttendMaxSplitBlocks / 2), 8);
-    bool split = false;
-    for (int i = 0; i < a.n_seg; ++i) split |= a.seg[i].n_split > 1;
-    if (split) {
-      const mag_status st = attend_workspace(c);
-      if (st != MAG_OK) return st;
-    }
-    a.part = c->at_part;
-    a.part_ml = c->at_ml;
-    a.arrivals = c->at_arrivals;
-    CUDA_TRY(c, launch_attend_few(L, a, tile_rows));
+    if (!a.n_seg) continue;
+    CUDA_TRY(c, many ? launch_attend_tc(L, a, c->n_sm) : launch_attend_few(L, a, c->n_sm, most <= 8 ? 8 : 16));
   }
   return MAG_OK;
 }
