@@ -445,6 +445,26 @@ def test_sample_ties(dtype):
 
 
 @pytest.mark.parametrize("dtype", [np.float16, np.float32])
+@pytest.mark.parametrize("rows,vocab", [(1, 128256), (3, 20000), (160, 9000)])
+def test_sample_crowds(dtype, rows, vocab):
+    """Thousands of tokens within a hair of each other, or equal, at and below the top: cuts and draws inside them."""
+    rng = np.random.default_rng(vocab)
+    flat = np.full((rows, vocab), 1.5, dtype)
+    steps = (rng.integers(0, 4, (rows, vocab)) * 0.5).astype(dtype)
+    peak = steps.copy()
+    peak[:, vocab // 3] = 9.0
+    narrow = rows_of(rng, rows, vocab, dtype, std=1e-3)
+    for x in (flat, steps, peak, narrow):
+        sample_case(x, seed=1)
+        sample_case(x, k=vocab // 2, seed=2)
+        sample_case(x, t=0.7, k=vocab - 1, p=0.6, seed=3)
+        sample_case(x, t=2.0, p=0.3, m=0.4, seed=4)
+        sample_case(x, t=1e4, p=0.9, seed=5)
+        sample_case(x, t=0.05, k=3000, m=0.9, seed=6)
+        sample_case(x, k=1000, p=0.99, seed=7)
+
+
+@pytest.mark.parametrize("dtype", [np.float16, np.float32])
 def test_sample_extremes(dtype):
     rng = np.random.default_rng(12)
     inf, nan = np.inf, np.nan
