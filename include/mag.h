@@ -325,7 +325,7 @@ typedef struct mag_sample_params {
  * the token's index, -1 for a row with no token to draw (none allowed, or every logit NaN or -inf; those are never
  * drawn); prob_dev[row] (may be null) its share of the kept w, NaN for a row without a token. Infinite
  * logits share all the weight. p may be null (temperature 1, no cuts).
- * Errors: INVALID_ARG, UNSUPPORTED (vocab above 589,824 in fp16, 294,912 in fp32), CUDA. */
+ * Errors: INVALID_ARG, UNSUPPORTED (vocab above 540,672 in fp16, 270,336 in fp32), CUDA. */
 mag_status mag_sample(const void* logits_dev, int32_t logits_type, int32_t rows, int32_t vocab, int64_t ld,
                       const mag_sample_params* p, const float* uniform_dev, int32_t* token_dev, float* prob_dev,
                       void* cuda_stream);

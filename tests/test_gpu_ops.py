@@ -392,8 +392,10 @@ def sample_case(logits, t=None, k=None, p=None, m=None, u=None, allowed=None, se
         ref, rp = sample_reference(logits[r], at(t, r, 1.0), int(at(k, r, 0)), at(p, r, 1.0), at(m, r, 0.0), u[r],
                                    np.ones(vocab, bool) if allowed is None else allowed[r])
         assert got[r] == ref, (r, got[r], ref)
-        # the quotient of two 64-bit numbers good to 2^-33 and the rounding to fp32
-        assert (math.isnan(rp) and math.isnan(gp[r])) or abs(gp[r] - rp) <= rp * (2.0 ** -24 + 2.0 ** -31), (r, gp[r], rp)
+        # Rounded to fp32 (2^-24 of it) from a quotient whose terms are good to 2^-30 of themselves, and whose upper one is
+        # rounded to units of 2^-40 of the row's largest weight: off by 2^-41 of that, and the sum is at least that.
+        assert (math.isnan(rp) and math.isnan(gp[r])) or abs(gp[r] - rp) <= rp * (2.0 ** -24 + 2.0 ** -28) + 2.0 ** -41, (
+            r, gp[r], rp)
     return got, gp
 
 
@@ -403,7 +405,7 @@ def rows_of(rng, rows, vocab, dtype, std=2.5):
 
 @pytest.mark.parametrize("dtype", [np.float16, np.float32])
 @pytest.mark.parametrize("rows,vocab", [(1, 1), (3, 2), (2, 31), (5, 33), (4, 1000), (1, 5001), (200, 777), (2, 128256),
-                                        (20, 20000)])
+                                        (20, 20000), (30, 1), (160, 40), (22, 128256), (5, 200000)])
 def test_sample_cuts(dtype, rows, vocab):
     rng = np.random.default_rng(rows + vocab)
     x = rows_of(rng, rows, vocab, dtype)
@@ -420,17 +422,20 @@ def test_sample_cuts(dtype, rows, vocab):
 def test_sample_strides_and_masks(dtype):
     rng = np.random.default_rng(9)
     for ld in (501, 508, 640):
-        x = rows_of(rng, 6, 501, dtype)
-        allowed = rng.random((6, 501)) < np.array([[1.0], [0.5], [0.01], [0.0], [0.9], [0.002]])
-        allowed[4, np.argsort(-x[4].astype(np.float64))[:5]] = False
-        sample_case(x, t=0.8, k=[0, 3, 0, 4, 10, 0], p=0.9, allowed=allowed, ld=ld, seed=ld)
+        for copies in (1, 5, 30):
+            x = rows_of(rng, 6 * copies, 501, dtype)
+            share = np.tile(np.array([[1.0], [0.5], [0.01], [0.0], [0.9], [0.002]]), (copies, 1))
+            allowed = rng.random((6 * copies, 501)) < share
+            allowed[4, np.argsort(-x[4].astype(np.float64))[:5]] = False
+            sample_case(x, t=0.8, k=[0, 3, 0, 4, 10, 0] * copies, p=0.9, allowed=allowed, ld=ld, seed=ld)
+            sample_case(x, t=0.8, m=[0, 0.1, 0, 0.9, 1e-3, 0] * copies, allowed=allowed, ld=ld, seed=ld)
 
 
 @pytest.mark.parametrize("dtype", [np.float16, np.float32])
 def test_sample_ties(dtype):
     """Equal logits go by index: in what top-k and top-p keep, and in the token that u picks."""
-    x = np.zeros((8, 4096), dtype)
-    u = [0.0, 0.25, 0.5, 0.999, 0.0, 0.5, 0.75, 1 - 2.0 ** -24]
+    x = np.zeros((24, 4096), dtype)
+    u = [0.0, 0.25, 0.5, 0.999, 0.0, 0.5, 0.75, 1 - 2.0 ** -24] * 3
     got, prob = sample_case(x, u=u)
     assert list(got) == [int(4096 * np.float32(v)) for v in u]
     got, _ = sample_case(x, k=16, u=u)
@@ -464,11 +469,42 @@ def test_sample_crowds(dtype, rows, vocab):
         sample_case(x, k=1000, p=0.99, seed=7)
 
 
+def test_sample_more_equal_tokens_than_16_bits_count():
+    """Rows of which most tokens are equal, many rows at a time: counts past 65,535, of even and odd patterns, at the top
+    and below it."""
+    rng = np.random.default_rng(5)
+    x = rows_of(rng, 24, 131000, np.float16)
+    for r in range(24):
+        few = rng.permutation(131000)[:65536 + 2000 * r]
+        x[r, few] = np.array([0x3C00 + r % 2], np.uint16).view(np.float16)[0] * (1 if r % 3 else -1)
+    x[::5, 77] = 14.0
+    sample_case(x, t=0.8, seed=1)
+    sample_case(x, t=1.2, k=rng.integers(0, 131000, 24), p=rng.uniform(0.1, 1.1, 24), m=rng.uniform(-0.1, 0.2, 24), seed=2)
+
+
+@pytest.mark.parametrize("copies", [1, 4, 20])
 @pytest.mark.parametrize("dtype", [np.float16, np.float32])
-def test_sample_extremes(dtype):
+def test_sample_extremes(dtype, copies):
     rng = np.random.default_rng(12)
+    nan = np.nan
+    x = np.concatenate([rows_of(rng, 9, 300, dtype)] * copies)
+    for at in range(0, 9 * copies, 9):
+        extreme_rows(x[at:at + 9], dtype)
+    got, prob = sample_case(x, seed=3)
+    assert got[0] == got[1] == -1 and got[2] in (5, 17, 200)
+    for t in (0.0, -1.0, nan, 1e-30, 1e-6, 1e6, 1e30):
+        sample_case(x, t=t, seed=4)
+    for p in (0.0, -3.0, 1e-9, 1.0, 5.0):
+        sample_case(x, p=p, seed=5)
+    for m in (2.0, 1.0, -1.0, 0.999, 1e-9):
+        sample_case(x, m=m, seed=6)
+    sample_case(x, k=-5, seed=7)
+    sample_case(x, k=2 ** 31 - 1, seed=8)
+    sample_case(x, k=7, m=0.5, seed=9)
+
+
+def extreme_rows(x, dtype):
     inf, nan = np.inf, np.nan
-    x = rows_of(rng, 9, 300, dtype)
     x[0, :] = -inf
     x[1, :] = nan
     x[2, [5, 17, 200]] = inf
@@ -479,16 +515,6 @@ def test_sample_extremes(dtype):
     x[6, 100:] = -inf
     x[7, ::2] = 60000.0
     x[7, 1::2] = 6e-8
-    got, prob = sample_case(x, seed=3)
-    assert got[0] == got[1] == -1 and got[2] in (5, 17, 200)
-    for t in (0.0, -1.0, nan, 1e-30, 1e-6, 1e6, 1e30):
-        sample_case(x, t=t, seed=4)
-    for p in (0.0, -3.0, 1e-9, 1.0, 5.0, nan):
-        sample_case(x, p=1.0 if math.isnan(p) else p, seed=5)
-    for m in (2.0, 1.0, -1.0, 0.999, 1e-9):
-        sample_case(x, m=m, seed=6)
-    sample_case(x, k=-5, seed=7)
-    sample_case(x, k=2 ** 31 - 1, seed=8)
 
 
 def test_sample_shares_of_many_draws():

@@ -25,9 +25,9 @@ def test_sample_refusals(lib):
                 dict(logits=None), dict(uniform=None), dict(token=None), dict(logits=x + 1),
                 dict(logits=x + 2, dtype=mag.LOGITS_F32)):
         assert call(**bad) == mag.ERR_INVALID_ARG, bad
-    assert call(vocab=589825, ld=589825) == mag.ERR_UNSUPPORTED
-    assert call(vocab=294913, ld=294913, dtype=mag.LOGITS_F32) == mag.ERR_UNSUPPORTED
-    assert call(rows=0, vocab=589824, ld=589824) == mag.OK
+    assert call(vocab=540673, ld=540673) == mag.ERR_UNSUPPORTED
+    assert call(vocab=270337, ld=270337, dtype=mag.LOGITS_F32) == mag.ERR_UNSUPPORTED
+    assert call(rows=0, vocab=540672, ld=540672) == mag.OK
 
 
 def test_null_context(lib):
