@@ -983,14 +983,17 @@ class CountedRow {
     }
     infinite_ = mx == INFINITY;  // infinite logits share all the weight
     w_ = Weight{infinite_ ? 0.f : mx, g.kh, g.kl, sm_.table};
-    if (add_up() != tokens) return false;
+    if (add_counts() != tokens) return false;
+    const bool use_k = g.top_k && sm_.cn[kOrdered] > (uint32_t)g.top_k;
+    if (use_k) find_chunk(true, g.top_k);
+    add_weights(use_k ? (int)sm_.chunk : kOrdered - 1);
 
     // the kept prefix, as its weight and last token's (chunk, place among the chunk's)
     u64 total = sm_.cw[kOrdered];
     Place end;
     end.key = 0;  // here: the order of the last kept pattern, larger is later; 0: everything
     bool cut = false;
-    if (g.top_k && sm_.cn[kOrdered] > (uint32_t)g.top_k) {
+    if (use_k) {
       end = find(true, g.top_k);
       total = end.above_w + end.tie * weight(end.index);
       cut = true;
@@ -1012,7 +1015,7 @@ class CountedRow {
   }
 
  private:
-  // f(8 patterns, -0 as 0, which of them may be drawn, first token) over the row, 2 runs of 8 in flight per thread.
+  // f(8 patterns in pairs, which of them may be drawn, first token) over the row, 4 runs of 8 in flight per thread.
   template <typename F>
   __device__ __forceinline__ void runs(F f) const {
     constexpr int U = 4;
@@ -1040,9 +1043,7 @@ class CountedRow {
 #pragma unroll
       for (int k = 0; k < U; ++k) {
         if (ok[k] == 0) continue;
-        const __half2 zero = __half2half2(__ushort_as_half(0));
-        const uint32_t w[4] = {h2_as_u32(__hadd2(u32_as_h2(v[k].x), zero)), h2_as_u32(__hadd2(u32_as_h2(v[k].y), zero)),
-                               h2_as_u32(__hadd2(u32_as_h2(v[k].z), zero)), h2_as_u32(__hadd2(u32_as_h2(v[k].w), zero))};
+        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
         f(w, ok[k], (c0 + k * kCountThreads) * 8);
       }
     }
@@ -1052,7 +1053,10 @@ class CountedRow {
   }
   // Counts the row's tokens by pattern; this thread's tokens that may be drawn, and its largest logits.
   __device__ void tokens_(uint32_t* n, __half2* top) {
-    runs([&](const uint32_t (&w)[4], uint32_t ok, int) {
+    runs([&](const uint32_t (&raw)[4], uint32_t ok, int) {
+      uint32_t w[4];  // -0 as 0
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = h2_as_u32(__hadd2(u32_as_h2(raw[i]), u32_as_h2(0u)));
       *n += __popc(ok);
       if (ok == 0xFFu) {
 #pragma unroll
@@ -1088,36 +1092,53 @@ class CountedRow {
     return w_.template value<false>(x);
   }
 
-  // Every chunk's tokens and weight, as running sums in falling order; the tokens counted, of any pattern.
-  __device__ uint32_t add_up() {
+  // Every ordered chunk's tokens as running sums, in falling order; the tokens counted, of any pattern.
+  __device__ uint32_t add_counts() {
     uint32_t counted = 0;
     for (int q = warp_; q < kChunks; q += kCountThreads / 32) {  // patterns 64 q .. 64 q + 63, two a lane
-      const uint32_t c = sm_.count[q * 32 + lane_], c0 = c & 0xFFFFu, c1 = c >> 16;
+      const uint32_t c = sm_.count[q * 32 + lane_];
       const int o = q <= 496 ? 496 - q : (q >= 512 && q < 1008 ? q - 15 : -1);
-      u64 w = 0;
-      uint32_t n = __reduce_add_sync(0xffffffffu, c0 + c1);
+      uint32_t n = __reduce_add_sync(0xffffffffu, (c & 0xFFFFu) + (c >> 16));
       counted += n;
-      if (o >= 0 && n) {
-        const uint32_t p = q * 64 + 2 * lane_;
-        if (q == 496) n = __reduce_add_sync(0xffffffffu, lane_ == 0 ? c0 : 0);  // +inf; the others are NaN
-        if (q != 496 || lane_ == 0) w = c0 * weight(p) + (q == 496 ? 0 : c1 * weight(p + 1));
-#pragma unroll
-        for (int k = 16; k; k >>= 1) w += __shfl_xor_sync(0xffffffffu, w, k);
-      }
-      if (o >= 0 && lane_ == 0) sm_.cw[o] = w, sm_.cn[o] = n;
+      if (q == 496) n = __shfl_sync(0xffffffffu, c, 0) & 0xFFFFu;  // +inf; the chunk's others are NaN
+      if (o >= 0 && lane_ == 0) sm_.cn[o] = n;
     }
     if (lane_ == 0) sm_.tiles[warp_] = counted;
     __syncthreads();
     counted = __reduce_add_sync(0xffffffffu, sm_.tiles[lane_]);
     uint32_t n = tid_ < kOrdered ? sm_.cn[tid_] : 0;
-    u64 w = tid_ < kOrdered ? sm_.cw[tid_] : 0;
+    u64 none = 0;
     const uint32_t n0 = n;
-    const u64 w0 = w;
-    scan(n, w);
-    if (tid_ < kOrdered) sm_.cn[tid_] = n - n0, sm_.cw[tid_] = w - w0;
-    if (tid_ == kOrdered) sm_.cn[tid_] = n, sm_.cw[tid_] = w;
+    scan(n, none);
+    if (tid_ < kOrdered) sm_.cn[tid_] = n - n0;
+    if (tid_ == kOrdered) sm_.cn[tid_] = n;
     __syncthreads();
     return counted;
+  }
+  // The weights of the chunks up to `last` likewise (the others as if they weighed nothing).
+  __device__ void add_weights(int last) {
+    for (int o = warp_; o < kOrdered; o += kCountThreads / 32) {
+      u64 w = 0;
+      if (o <= last && sm_.cn[o + 1] != sm_.cn[o]) {
+        const uint32_t p = pattern_of(o, 0) & ~63u, c = sm_.count[(p >> 1) + lane_];
+        if (o != 0 || lane_ == 0) w = (c & 0xFFFFu) * weight(p + 2 * lane_);
+        if (o != 0) w += (c >> 16) * weight(p + 2 * lane_ + 1);
+        // below 2^58: the warp's sum by parts of 21 bits
+        const uint32_t a = __reduce_add_sync(0xffffffffu, (uint32_t)w & 0x1FFFFFu);
+        const uint32_t b = __reduce_add_sync(0xffffffffu, (uint32_t)(w >> 21) & 0x1FFFFFu);
+        const uint32_t h = __reduce_add_sync(0xffffffffu, (uint32_t)(w >> 42));
+        w = a + ((u64)b << 21) + ((u64)h << 42);
+      }
+      if (lane_ == 0) sm_.cw[o] = w;
+    }
+    __syncthreads();
+    uint32_t none = 0;
+    u64 w = tid_ < kOrdered ? sm_.cw[tid_] : 0;
+    const u64 w0 = w;
+    scan(none, w);
+    if (tid_ < kOrdered) sm_.cw[tid_] = w - w0;
+    if (tid_ == kOrdered) sm_.cw[tid_] = w;
+    __syncthreads();
   }
   __device__ void scan(uint32_t& c, u64& w) {
 #pragma unroll
@@ -1137,14 +1158,18 @@ class CountedRow {
     __syncthreads();
   }
 
-  // The place where the running count or weight reaches target, which the row's does: index is the pattern here, tie its
-  // token's number, above_w the weight of the patterns above.
-  __device__ Place find(bool by_count, u64 target) {
+  // The chunk in which the running count or weight reaches target.
+  __device__ void find_chunk(bool by_count, u64 target) {
     if (tid_ < kOrdered) {
       const u64 lo = by_count ? sm_.cn[tid_] : sm_.cw[tid_], hi = by_count ? sm_.cn[tid_ + 1] : sm_.cw[tid_ + 1];
       if (lo < target && target <= hi) sm_.chunk = tid_;
     }
     __syncthreads();
+  }
+  // The place where the running count or weight reaches target, which the row's does: index is the pattern here, tie its
+  // token's number, above_w the weight of the patterns above.
+  __device__ Place find(bool by_count, u64 target) {
+    find_chunk(by_count, target);
     if (warp_ == 0) {  // two patterns a lane
       const int c = sm_.chunk;
       const uint32_t p0 = pattern_of(c, 2 * lane_), p1 = pattern_of(c, 2 * lane_ + 1);
@@ -1222,9 +1247,16 @@ class CountedRow {
     const int n_tiles = (a_.vocab + 255) / 256;
     for (int i = tid_; i < kCountThreads; i += kCountThreads) sm_.tiles[i] = 0;
     __syncthreads();
-    const uint32_t two = pattern * 0x10001u;
+    const __half2 wanted = u32_as_h2(pattern * 0x10001u);
     runs([&](const uint32_t (&v)[4], uint32_t ok, int i0) {
-      const uint32_t m = matches(v, two) & ok;
+      uint32_t eq[4];  // all ones in the halves that are equal
+#pragma unroll
+      for (int i = 0; i < 4; ++i) eq[i] = __heq2_mask(u32_as_h2(v[i]), wanted);
+      if (!(eq[0] | eq[1] | eq[2] | eq[3])) return;
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m |= (eq[i] & 1u) << (2 * i) | (eq[i] >> 31) << (2 * i + 1);
+      m &= ok;
       if (m) atomicAdd(&sm_.tiles[i0 >> 8], __popc(m));
     });
     __syncthreads();
@@ -1257,15 +1289,6 @@ class CountedRow {
       }
     }
   }
-  __device__ static uint32_t matches(const uint32_t (&v)[4], uint32_t two) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t d = v[i] ^ two;
-      m |= (uint32_t)((d & 0xFFFFu) == 0) << (2 * i) | (uint32_t)((d >> 16) == 0) << (2 * i + 1);
-    }
-    return m;
-  }
   __device__ void write(int32_t index, u64 w, u64 total) {
     a_.token[row_] = index;
     if (a_.prob) a_.prob[row_] = index < 0 ? __int_as_float(0x7fc00000) : quotient(w, total);
@@ -1283,7 +1306,9 @@ class CountedRow {
 
 __global__ void __launch_bounds__(kCountThreads, 1) sample_counted_kernel(const __grid_constant__ SampleArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  if (CountedRow(a, *reinterpret_cast<CountSmem*>(smem_raw)).run()) return;
+  // a row with a top-k that the partial maxima bring down to a list needs no count (256 rows of 128,256: 35 us, 57 counted)
+  const int k = a.top_k ? a.top_k[blockIdx.x] : 0;
+  if ((k <= 0 || k > kCap / 2) && CountedRow(a, *reinterpret_cast<CountSmem*>(smem_raw)).run()) return;
   __syncthreads();
   Sampler<__half, 1, kCountThreads, false>(a, *reinterpret_cast<SampleSmem<1>*>(smem_raw), nullptr).run();
 }
