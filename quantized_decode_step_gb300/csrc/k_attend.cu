@@ -517,28 +517,67 @@ cudaError_t launch_few_kv(const Launch& L, const AttendArgs& a, const AttendShar
 
 }  // namespace
 
-// The sessions' units, and every block's equal share of their steps: block b begins at step total b / n of all
-// units in order.
-void attend_shares(AttendArgs& a, int tile_rows, int step_keys, int max_blocks, int min_steps, AttendShares& sh) {
+// The sessions' units, and every block's share of their steps, in order. Equal shares, block b beginning at step
+// total b / n, keep every SM busy to the end, but most blocks then work on two units or more; where there are no more
+// units than blocks and whole parts of units take a block at most `piece` steps longer, it gets one part of one unit.
+void attend_shares(AttendArgs& a, int tile_rows, int step_keys, int max_blocks, int min_steps, int piece,
+                   AttendShares& sh) {
   int64_t total = 0, units = 0;
   int p_lo, p_hi, key0;
   auto steps = [&](const AttendSeg& s, int tile) {
     return attend_unit_steps(s.pos0, s.n_tok * a.group, a.group, a.window, tile * tile_rows, tile_rows, step_keys, p_lo,
                              p_hi, key0);
   };
+  max_blocks = std::min(max_blocks, kAttendMaxShares);
   int64_t per_head[MAG_MAX_BATCH];
+  int most = 1;
   for (int i = 0; i < a.n_seg; ++i) {
     AttendSeg& s = a.seg[i];
-    s.n_tiles = (s.n_tok * a.group + tile_rows - 1) / tile_rows;
+    s.n_tiles = (int)(((int64_t)s.n_tok * a.group + tile_rows - 1) / tile_rows);
     s.unit0 = (int32_t)units;
     units += (int64_t)s.n_tiles * a.n_kv_heads;
     per_head[i] = 0;
-    for (int j = 0; j < s.n_tiles; ++j) per_head[i] += steps(s, j);
+    for (int j = 0; j < s.n_tiles; ++j) {
+      const int n = steps(s, j);
+      per_head[i] += n;
+      most = std::max(most, n);
+    }
     total += per_head[i] * a.n_kv_heads;
   }
   a.n_units = (int32_t)units;
-  sh.n = (int32_t)std::max<int64_t>(
-      1, std::min<int64_t>(std::min(max_blocks, kAttendMaxShares), (total + min_steps - 1) / min_steps));
+  const int64_t equal = std::max<int64_t>(min_steps, (total + max_blocks - 1) / max_blocks);
+  if (units <= max_blocks) {
+    // the shortest parts, all of a unit alike, that make no more blocks than there may be
+    auto blocks = [&](int64_t len) {
+      int64_t n = 0;
+      for (int i = 0; i < a.n_seg; ++i)
+        for (int j = 0; j < a.seg[i].n_tiles; ++j) n += (steps(a.seg[i], j) + len - 1) / len * a.n_kv_heads;
+      return n;
+    };
+    int64_t lo = std::min<int64_t>(min_steps, most), hi = most;  // hi: one part a unit
+    while (lo < hi) {
+      const int64_t mid = (lo + hi) / 2;
+      if (blocks(mid) <= max_blocks) hi = mid;
+      else lo = mid + 1;
+    }
+    if (lo <= equal + piece) {
+      int b = 0;
+      for (int i = 0; i < a.n_seg; ++i)
+        for (int h = 0; h < a.n_kv_heads; ++h)
+          for (int j = 0; j < a.seg[i].n_tiles; ++j) {
+            const int64_t n = steps(a.seg[i], j), parts = (n + lo - 1) / lo;
+            for (int64_t k = 0; k < parts; ++k, ++b) {
+              sh.unit[b] = a.seg[i].unit0 + h * a.seg[i].n_tiles + j;
+              sh.step[b] = (int32_t)(n * k / parts);
+            }
+          }
+      sh.n = b;
+      sh.unit[b] = a.n_units;
+      sh.step[b] = 0;
+      return;
+    }
+  }
+  sh.n = (int32_t)std::max<int64_t>(1, std::min<int64_t>(max_blocks, (total + min_steps - 1) / min_steps));
   int si = 0, head = 0, tile = 0;
   int64_t at = 0;
   for (int b = 0; b < sh.n; ++b) {
@@ -569,7 +608,7 @@ cudaError_t launch_attend_few(const Launch& L, AttendArgs& a, int n_sm, int tile
   if (a.n_seg < 1 || a.n_seg > MAG_MAX_BATCH || (tile_rows != 8 && tile_rows != 16)) return cudaErrorInvalidValue;
   // a block's share is at least a pool block for each of (about) its warps
   AttendShares sh;
-  attend_shares(a, tile_rows, 16, n_sm, 12, sh);
+  attend_shares(a, tile_rows, 16, n_sm, 12, 24, sh);
   return a.pool.head_dim == 64 ? launch_few_kv<64>(L, a, sh, tile_rows) : launch_few_kv<128>(L, a, sh, tile_rows);
 }
 

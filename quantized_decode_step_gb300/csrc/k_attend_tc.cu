@@ -24,158 +24,15 @@
 //
 // Every wait is bounded; a role whose wait gives up sets a bit in the error word and leaves, after its own copies
 // and MMAs in flight.
-#include <cuda.h>
-
 #include <algorithm>
 
-#include "kernels.h"
+#include "attend_tc.cuh"
 
 namespace mag {
 
 namespace {
 
-constexpr int kRows = 128, kKeys = 128;  // rows of a tile, keys of a step
-constexpr float kLazy = 8.0f, kShift = 7.0f;
-constexpr uint32_t kErrAttend = 512u;
-
-__device__ __forceinline__ uint32_t su32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-__device__ __forceinline__ void mb_init(uint64_t* b, uint32_t n) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(su32(b)), "r"(n) : "memory");
-}
-__device__ __forceinline__ void mb_expect(uint64_t* b, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(b)), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void mb_arrive(uint64_t* b) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(b)) : "memory");
-}
-__device__ __forceinline__ bool mb_wait(uint64_t* b, uint32_t par) {
-  for (uint32_t i = 0; i < kWaitPolls; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(su32(b)), "r"(par)
-        : "memory");
-    if (ok) return true;
-  }
-  return false;
-}
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
-          "r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(su32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(su32(bar))
-               : "memory");
-}
-// Shared-memory operand of 128-byte rows with 128-byte swizzle, 8-row groups 1024 bytes apart. K-major (Q, K): the
-// row is the M or N index. MN-major (V): the row is the contraction index, 64 dimensions long, and the
-// next 64 dimensions lie `next` bytes further (the leading-dimension offset).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t next) {
-  uint64_t d = (static_cast<uint64_t>(addr) & 0x3FFFFull) >> 4;
-  d |= static_cast<uint64_t>(next >> 4) << 16;
-  d |= (1024ull >> 4) << 32;
-  d |= 1ull << 46;
-  d |= 2ull << 61;
-  return d;
-}
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(bar))
-               : "memory");
-}
-__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// 32 consecutive columns of this thread's lane, not waited for.
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, float* v) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(v);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(addr));
-}
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const float* v) {
-  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-struct F2 {
-  unsigned long long v;
-};
-__device__ __forceinline__ F2 f2(float a, float b) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack(F2 x, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v));
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-__device__ __forceinline__ void wg_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+using namespace tc;
 
 // ---------------------------------------------------------------- shapes
 template <int D, int KV>
@@ -190,7 +47,7 @@ struct Cfg {
   static constexpr int kThreads = KV == 0 ? 384 : 512;
   // registers: 384 x 168 or 512 x 128 at launch
   static constexpr int kRegsSoftmax = KV == 0 ? 200 : 184, kRegsOther = KV == 0 ? 104 : 72;
-  static constexpr int kBars = 2 * kStages + 2 * kRaw + 9;
+  static constexpr int kBars = 2 * kStages + 2 * kRaw + 11;
   static constexpr int kSmem = 2 * kTile + kStages * kTile + kRaw * kRawBytes + kBars * 8 + 64 + 1024;
 };
 
@@ -277,7 +134,8 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
   uint64_t* s_full = q_full + 2;   // [2]: S of the tile is in tensor memory (and o holds every earlier step)
   uint64_t* p_full = s_full + 2;   // [2]: P is
   uint64_t* o_full = p_full + 2;   // [2]: o is final
-  uint64_t* mma_done = o_full + 2;
+  uint64_t* joined = o_full + 2;   // [2]: the tile's four softmax warps
+  uint64_t* mma_done = joined + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);  // and [1], [2]: the tiles' last-arrival flags
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PoolGeom& P = a.pool;
@@ -296,6 +154,7 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
       mb_init(s_full + i, 1);
       mb_init(p_full + i, 4);
       mb_init(o_full + i, 1);
+      mb_init(joined + i, 4);
     }
     mb_init(mma_done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -508,7 +367,12 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
     const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale: -q with its absolute value
     const bool zero = a.scale_log2 == 0.f;                        // every score 0
     const int G = a.group;
-    int cnt = 0, n_o = 0;
+    int cnt = 0, n_o = 0, n_join = 0;
+    auto all = [&] {
+      const bool ok = join(joined + t, n_join);
+      if (!ok && lane == 0) atomicOr(a.err, kErrAttend);
+      return ok;
+    };
     for_share(a, sh, [&](const Unit& x, int u, int s0, int s1) {
       // Q of the tile into its swizzled place (every MMA that read the previous one is done)
       if (x.n_rows - x.r0 <= t * kRows) return true;  // no such tile
@@ -654,7 +518,7 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
       int b0 = blockIdx.x, b1 = blockIdx.x;
       while (sh.unit[b0] == u && sh.step[b0] > 0) --b0;
       while (sh.unit[b1 + 1] == u && sh.step[b1 + 1] < x.n_steps) ++b1;
-      wg_sync(1 + t);
+      if (!all()) return false;
       if (row == 0) {
         uint32_t* cnt_p = a.arrivals + 2 * b0 + t;
         const uint32_t prev = atomicAdd(cnt_p, 1u);
@@ -662,7 +526,7 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
         if (last) *cnt_p = 0;  // for the next launch
         tmem_slot[1 + t] = last;
       }
-      wg_sync(1 + t);
+      if (!all()) return false;
       if (!tmem_slot[1 + t]) return true;
       __threadfence();
       auto part_of = [&](int b) {
@@ -670,7 +534,9 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
         return a.part + (int64_t)(2 * slot + t) * kPart + row;
       };
       float mt = -INFINITY, lt = 0.f;
+#pragma unroll 4
       for (int b = b0; b <= b1; ++b) mt = fmaxf(mt, __ldcg(part_of(b) + D * kRows));
+#pragma unroll 4
       for (int b = b0; b <= b1; ++b) {
         const float mb = __ldcg(part_of(b) + D * kRows);
         lt = fmaf(mb == -INFINITY ? 0.f : ex2(mb - mt), __ldcg(part_of(b) + (D + 1) * kRows), lt);
@@ -681,6 +547,7 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
         float o[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = 0.f;
+#pragma unroll 2
         for (int b = b0; b <= b1; ++b) {
           const float* pb = part_of(b);
           const float mb = __ldcg(pb + D * kRows);
@@ -698,39 +565,14 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = [] {
-    cudaDriverEntryPointQueryResult q;
-    void* p = nullptr;
-    return cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-                   q == cudaDriverEntryPointSuccess
-               ? reinterpret_cast<EncodeTiledFn>(p)
-               : nullptr;
-  }();
-  return fn;
-}
-
 template <int D, int KV>
 cudaError_t launch_tc_t(const Launch& L, const AttendArgs& a, const AttendShares& sh) {
   using C = Cfg<D, KV>;
   static_assert(C::kSmem <= 227 * 1024, "shared memory");
   alignas(64) CUtensorMap map = {};
-  if (KV == 0) {  // the layer's pool blocks as rows of D values: [block][K, V][head][16]
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return cudaErrorNotSupported;
-    cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)a.pool.pool_blocks * 2 * a.pool.n_kv_heads * 16};
-    cuuint64_t strides[1] = {(cuuint64_t)D * 2};
-    cuuint32_t box[2] = {64, 16}, es[2] = {1, 1};
-    void* base = a.pool.base + (int64_t)a.layer * a.pool.pool_blocks * a.pool.block_bytes;
-    if (fn(&map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return cudaErrorInvalidValue;
-  }
-  cudaError_t e = cudaFuncSetAttribute(attend_tc_kernel<D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  cudaError_t e = KV == 0 ? pool_map(&map, a) : cudaSuccess;
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(attend_tc_kernel<D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   attend_tc_kernel<D, KV><<<sh.n, C::kThreads, C::kSmem, L.stream>>>(map, a, sh);
   if (L.counter) ++*L.counter;
@@ -756,7 +598,7 @@ cudaError_t launch_attend_tc(const Launch& L, AttendArgs& a, int n_sm) {
   if (a.n_seg < 1 || a.n_seg > MAG_MAX_BATCH) return cudaErrorInvalidValue;
   // every block at least two steps: a merge costs about as much
   AttendShares sh;
-  attend_shares(a, 2 * kRows, kKeys, n_sm, 2, sh);
+  attend_shares(a, 2 * kRows, kKeys, n_sm, 2, 4, sh);
   return a.pool.head_dim == 64 ? launch_tc_kv<64>(L, a, sh) : launch_tc_kv<128>(L, a, sh);
 }
 

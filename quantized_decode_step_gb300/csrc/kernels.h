@@ -278,8 +278,8 @@ cudaError_t launch_kv_read(const Launch& L, const KvReadArgs& a, int n_layers);
 
 // Causal grouped-query attention of the sessions' newest tokens over the pool. The G query heads of a KV head and
 // the tokens of a session are packed into rows, row t G + g, cut into tiles; a unit is one (session, KV head, tile)
-// over its keys in steps. The units' steps, in order, are dealt out to the blocks in equal shares; blocks that
-// share a unit leave (m, l, o) in the workspace for the last of them to merge.
+// over its keys in steps. The units' steps, in order, are dealt out to the blocks in shares; blocks that share a unit
+// leave (m, l, o) in the workspace for the last of them to merge.
 struct AttendSeg {
   int32_t row0, n_tok, pos0, sess;  // as KvSeg
   int32_t unit0, n_tiles;           // units of this session: unit0 + head * n_tiles + tile
@@ -317,13 +317,16 @@ __host__ __device__ inline int attend_unit_steps(int pos0, int n_rows, int G, in
   key0 = first & ~15;
   return (p_hi - key0) / step_keys + 1;
 }
-void attend_shares(AttendArgs& a, int tile_rows, int step_keys, int max_blocks, int min_steps, AttendShares& sh);
+void attend_shares(AttendArgs& a, int tile_rows, int step_keys, int max_blocks, int min_steps, int piece,
+                   AttendShares& sh);
 // Workspace: two cut pieces a block, of 16 rows of 128 values, or of two tiles of 128 rows of 128 values and (m, l).
 constexpr size_t kAttendPartFloats = (size_t)kAttendMaxShares * 2 * 2 * 130 * 128;
 constexpr size_t kAttendMlFloats = (size_t)kAttendMaxShares * 2 * 16 * 2;
 constexpr size_t kAttendArrivals = 2 * kAttendMaxShares;
 // Few rows: tiles of 8 or 16 rows.
 cudaError_t launch_attend_few(const Launch& L, AttendArgs& a, int n_sm, int tile_rows);
+// Up to 128 rows of many keys (tcgen05).
+cudaError_t launch_attend_stream(const Launch& L, AttendArgs& a, int n_sm);
 // Many rows (tcgen05); false where the pool is too large for it.
 bool attend_tc_fits(const AttendArgs& a);
 cudaError_t launch_attend_tc(const Launch& L, AttendArgs& a, int n_sm);

@@ -86,7 +86,11 @@ static mag_status attend_workspace(mag_ctx* c) {
   return MAG_OK;
 }
 
-constexpr int kFewRows = 16;  // most packed rows of a session for the few-row kernel
+// Which kernel a session goes to, by its packed rows (tokens times query heads per KV head): up to kFewRows to the
+// register kernel, up to 128 (one tile) to the streaming one, others to the two-tile one. Of many keys the streaming
+// kernel is faster with few rows as well.
+constexpr int kFewRows = 16, kStreamRows = 128;
+constexpr int64_t kFewBlocks = 1 << 30;
 
 static mag_status run_attend(mag_ctx* c, int32_t layer, const KvRows& rows, const void* q, int64_t ldq, void* out, int64_t ldo,
                       int32_t window, float scale) {
@@ -110,19 +114,27 @@ static mag_status run_attend(mag_ctx* c, int32_t layer, const KvRows& rows, cons
   a.arrivals = c->at_arrivals;
   const Launch L{c->stream, false, nullptr};
   const bool tc = attend_tc_fits(a);
-  // sessions of up to kFewRows packed rows, then the others
-  for (int many = 0; many < 2; ++many) {
+  int64_t few_blocks = 0;  // pool blocks of the sessions of few rows, over the KV heads
+  for (int i = 0; i < rows.n_seg; ++i) {
+    const KvSeg& s = rows.seg[i];
+    int64_t keys = s.pos0 + s.n_tok;
+    if (window) keys = std::min<int64_t>(keys, (int64_t)window + s.n_tok);
+    if ((int64_t)s.n_tok * c->G <= kFewRows) few_blocks += (keys + 15) / 16 * c->Hkv;
+  }
+  const int few_rows = !tc ? INT32_MAX : (few_blocks <= kFewBlocks ? kFewRows : 0);
+  for (int kind = 0; kind < 3; ++kind) {
     int64_t most = 0;
     a.n_seg = 0;
     for (int i = 0; i < rows.n_seg; ++i) {
       const KvSeg& s = rows.seg[i];
       const int64_t n = (int64_t)s.n_tok * c->G;
-      if ((tc && n > kFewRows) != (many != 0)) continue;
+      if ((n <= few_rows ? 0 : (n <= kStreamRows ? 1 : 2)) != kind) continue;
       a.seg[a.n_seg++] = AttendSeg{s.row0, s.n_tok, s.pos0, s.sess, 0, 0};
       most = std::max(most, n);
     }
     if (!a.n_seg) continue;
-    CUDA_TRY(c, many ? launch_attend_tc(L, a, c->n_sm) : launch_attend_few(L, a, c->n_sm, most <= 8 ? 8 : 16));
+    CUDA_TRY(c, kind == 0 ? launch_attend_few(L, a, c->n_sm, most <= 8 ? 8 : 16)
+                          : (kind == 1 ? launch_attend_stream(L, a, c->n_sm) : launch_attend_tc(L, a, c->n_sm)));
   }
   return MAG_OK;
 }
