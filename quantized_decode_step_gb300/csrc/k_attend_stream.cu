@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
   uint64_t* o_full = p_full + 2;   // [2]: o is final
   uint64_t* joined = o_full + 2;   // the eight softmax warps
   uint64_t* mma_done = joined + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);  // and [1]: the last-arrival flag
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PoolGeom& P = a.pool;
 
@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const uint32_t tm_s = tmem, tm_o = tmem + 2 * kKeys;  // S (and P) of stream t at + 128 t, o of stream t at + 128 t
 
+  pdl_trigger();  // the merge kernel may be put in place; it waits for this grid's end
   if (warp == 0) {
     // ---- loader
     const uint8_t* layer_base = P.base + (int64_t)a.layer * P.pool_blocks * P.block_bytes;
@@ -360,6 +361,8 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
     const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale: -q with its absolute value
     const bool zero = a.scale_log2 == 0.f;                        // every score 0
     const int G = a.group;
+    const uint32_t g_inv = (uint32_t)(0xFFFFFFFFu / (uint32_t)G) + 1u;  // of G > 1: r / G is the high word of r g_inv for r < 2^28
+    auto token_of = [&](int r) { return G == 1 ? r : (int)__umulhi((uint32_t)r, g_inv); };
     int cnt = 0, n_o = 0, n_join = 0;
     auto all = [&] {
       const bool ok = join(joined, n_join);
@@ -370,12 +373,13 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
       // Q into its swizzled place (every MMA that read the previous one is done)
       constexpr int cpr = D / 8;  // 16-byte runs of a row
       const int rows32 = (x.live + 31) & ~31;  // the rows of warps that have any
+      const int c = wg & (cpr - 1);
+      const __half* qh = a.q + (int64_t)x.sg.row0 * a.ldq + (int64_t)x.head * G * D + 8 * c;
 #pragma unroll 4
       for (int i = wg; i < rows32 * cpr; i += 256) {
-        const int rr = i / cpr, c = i % cpr, r = x.r0 + rr;
+        const int rr = i / cpr, r = x.r0 + rr, tok = token_of(r);
         uint4 w = make_uint4(0, 0, 0, 0);
-        if (r < x.n_rows && !zero)
-          w = ldg_stream_u4(a.q + (int64_t)(x.sg.row0 + r / G) * a.ldq + (int64_t)(x.head * G + r % G) * D + 8 * c);
+        if (r < x.n_rows && !zero) w = ldg_stream_u4(qh + (int64_t)tok * a.ldq + (r - tok * G) * D);
         w.x ^= flip, w.y ^= flip, w.z ^= flip, w.w ^= flip;
         if (KV == 2)
           w = make_uint4(__byte_perm(w.x, w.z, 0x5410), __byte_perm(w.x, w.z, 0x7632), __byte_perm(w.y, w.w, 0x5410),
@@ -481,8 +485,7 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
       if (!all()) return false;
       const bool whole = s0 == 0 && s1 == x.n_steps;
       const int mine = 2 * (int)blockIdx.x + (u == sh.unit[blockIdx.x] ? 0 : 1);
-      // parts: [2 per block][tile rows][D], (m, l) behind all of them
-      float2* part_ml = reinterpret_cast<float2*>(a.part + (size_t)2 * kAttendMaxShares * kRows * D);
+      constexpr int kPart = (D + 2) * kRows;  // as k_attend_merge.cu reads it
       if (t == 0 && busy) {
         const float2 b = ml_b[row];
         const float mt = fmaxf(m, b.x);
@@ -490,7 +493,7 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
         const float lt = fmaf(fb, b.y, fa * l), inv = 1.0f / lt;
         const bool live = row < x.live;
         __half* dst = a.o + (int64_t)(x.sg.row0 + r / G) * a.ldo + (int64_t)(x.head * G + r % G) * D;
-        float* part = a.part + ((size_t)mine * kRows + row) * D;
+        float* part = a.part + (size_t)mine * kPart + row;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
@@ -505,69 +508,26 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = fmaf(fb, ob[i], o[i]);
           }
-          if (live) {
+          if (!whole) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) __stcg(part + (c + i) * kRows, o[i]);
+          } else if (live) {
 #pragma unroll
             for (int i = 0; i < 32; i += 8) {
-              if (whole) {
-                float y[8];
+              float y[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] = o[i + k] * inv;
-                *reinterpret_cast<uint4*>(dst + c + i) = pack8<KV>(y);
-              } else {
-                __stcg(reinterpret_cast<float4*>(part + c + i), make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
-                __stcg(reinterpret_cast<float4*>(part + c + i + 4), make_float4(o[i + 4], o[i + 5], o[i + 6], o[i + 7]));
-              }
+              for (int k = 0; k < 8; ++k) y[k] = o[i + k] * inv;
+              *reinterpret_cast<uint4*>(dst + c + i) = pack8<KV>(y);
             }
           }
         }
-        if (live && !whole) __stcg(part_ml + (size_t)mine * kRows + row, make_float2(mt, lt));
+        if (!whole) {
+          __stcg(part + D * kRows, mt);
+          __stcg(part + (D + 1) * kRows, lt);
+        }
       }
       tc_before();
-      if (!whole) __threadfence();
       if (!all()) return false;  // o is read: the next piece may write it
-      if (whole) return true;
-      // ---- a cut unit: the last of its blocks to arrive adds the parts in order
-      int c0 = blockIdx.x, c1 = blockIdx.x;
-      while (sh.unit[c0] == u && sh.step[c0] > 0) --c0;
-      while (sh.unit[c1 + 1] == u && sh.step[c1 + 1] < x.n_steps) ++c1;
-      if (wg == 0) {
-        const uint32_t prev = atomicAdd(a.arrivals + c0, 1u);
-        const bool last = (int)prev == c1 - c0;
-        if (last) a.arrivals[c0] = 0;  // for the next launch
-        tmem_slot[1] = last;
-      }
-      if (!all()) return false;
-      if (!tmem_slot[1]) return true;
-      __threadfence();
-      auto slot_of = [&](int c) { return 2 * c + (u == sh.unit[c] ? 0 : 1); };
-      // 8 columns a lane, D / 8 lanes a row
-      constexpr int lpr = D / 8;
-      for (int rr = wg / lpr; rr < x.live; rr += 256 / lpr) {
-        const int c = (wg % lpr) * 8;
-        float mt = -INFINITY, lt = 0.f;
-#pragma unroll 8
-        for (int k = c0; k <= c1; ++k) mt = fmaxf(mt, __ldcg(part_ml + (size_t)slot_of(k) * kRows + rr).x);
-        float o[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = 0.f;
-#pragma unroll 4
-        for (int k = c0; k <= c1; ++k) {
-          const size_t at = (size_t)slot_of(k) * kRows + rr;
-          const float2 q = __ldcg(part_ml + at);
-          const float4 y0 = __ldcg(reinterpret_cast<const float4*>(a.part + at * D + c));
-          const float4 y1 = __ldcg(reinterpret_cast<const float4*>(a.part + at * D + c + 4));
-          const float f = q.x == -INFINITY ? 0.f : ex2(q.x - mt);
-          lt = fmaf(f, q.y, lt);
-          o[0] = fmaf(f, y0.x, o[0]), o[1] = fmaf(f, y0.y, o[1]), o[2] = fmaf(f, y0.z, o[2]), o[3] = fmaf(f, y0.w, o[3]);
-          o[4] = fmaf(f, y1.x, o[4]), o[5] = fmaf(f, y1.y, o[5]), o[6] = fmaf(f, y1.z, o[6]), o[7] = fmaf(f, y1.w, o[7]);
-        }
-        const float inv = 1.0f / lt;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] *= inv;
-        const int rq = x.r0 + rr;
-        *reinterpret_cast<uint4*>(a.o + (int64_t)(x.sg.row0 + rq / G) * a.ldo + (int64_t)(x.head * G + rq % G) * D + c) =
-            pack8<KV>(o);
-      }
       return true;
     });
   }
@@ -588,7 +548,8 @@ cudaError_t launch_stream_t(const Launch& L, const AttendArgs& a, const AttendSh
   if (e != cudaSuccess) return e;
   attend_stream_kernel<D, KV><<<sh.n, C::kThreads, C::kSmem, L.stream>>>(map, a, sh);
   if (L.counter) ++*L.counter;
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  return e == cudaSuccess ? launch_attend_merge(L, a, sh, 1, KV == 2) : e;
 }
 template <int D>
 cudaError_t launch_stream_kv(const Launch& L, const AttendArgs& a, const AttendShares& sh) {

@@ -8,8 +8,8 @@
 //
 // A unit is 256 rows (two tiles of 128) of one session and KV head over their keys in steps of 128. One block per
 // SM takes an equal share of all units' steps, in order, so that every SM works to the end whatever the causal
-// triangle leaves of the units; a unit cut by a share's end leaves (m, l, o) in the workspace, and the last of its
-// blocks to arrive adds the parts in order (the result does not depend on who was last).
+// triangle leaves of the units; a unit cut by a share's end leaves (m, l, o) in the workspace, whose parts a second
+// kernel (k_attend_merge.cu) puts together.
 //
 // Roles: one warp loads K and V of a step into a ring of swizzled tiles (FP16 by TMA, a 16-token pool block and 64
 // dimensions a copy; INT8 and INT4 as raw bytes that four warps expand to the fp16 values the pool reads
@@ -47,7 +47,7 @@ struct Cfg {
   static constexpr int kThreads = KV == 0 ? 384 : 512;
   // registers: 384 x 168 or 512 x 128 at launch
   static constexpr int kRegsSoftmax = KV == 0 ? 200 : 184, kRegsOther = KV == 0 ? 104 : 72;
-  static constexpr int kBars = 2 * kStages + 2 * kRaw + 11;
+  static constexpr int kBars = 2 * kStages + 2 * kRaw + 9;
   static constexpr int kSmem = 2 * kTile + kStages * kTile + kRaw * kRawBytes + kBars * 8 + 64 + 1024;
 };
 
@@ -134,9 +134,8 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
   uint64_t* s_full = q_full + 2;   // [2]: S of the tile is in tensor memory (and o holds every earlier step)
   uint64_t* p_full = s_full + 2;   // [2]: P is
   uint64_t* o_full = p_full + 2;   // [2]: o is final
-  uint64_t* joined = o_full + 2;   // [2]: the tile's four softmax warps
-  uint64_t* mma_done = joined + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);  // and [1], [2]: the tiles' last-arrival flags
+  uint64_t* mma_done = o_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PoolGeom& P = a.pool;
 
@@ -154,7 +153,6 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
       mb_init(s_full + i, 1);
       mb_init(p_full + i, 4);
       mb_init(o_full + i, 1);
-      mb_init(joined + i, 4);
     }
     mb_init(mma_done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -169,6 +167,7 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const uint32_t tm_s = tmem, tm_o = tmem + 2 * kKeys;  // S (and P) of tile t at + 128 t, o of tile t at + 128 t
 
+  pdl_trigger();  // the merge kernel may be put in place; it waits for this grid's end
   if (warp < 4) {
     regs_dec<C::kRegsOther>();
     if (warp == 0) {
@@ -367,26 +366,30 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
     const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale: -q with its absolute value
     const bool zero = a.scale_log2 == 0.f;                        // every score 0
     const int G = a.group;
-    int cnt = 0, n_o = 0, n_join = 0;
-    auto all = [&] {
-      const bool ok = join(joined + t, n_join);
-      if (!ok && lane == 0) atomicOr(a.err, kErrAttend);
-      return ok;
-    };
+    const uint32_t g_inv = (uint32_t)(0xFFFFFFFFu / (uint32_t)G) + 1u;  // of G > 1: r / G is the high word of r g_inv for r < 2^28
+    auto token_of = [&](int r) { return G == 1 ? r : (int)__umulhi((uint32_t)r, g_inv); };
+    int cnt = 0, n_o = 0;
     for_share(a, sh, [&](const Unit& x, int u, int s0, int s1) {
       // Q of the tile into its swizzled place (every MMA that read the previous one is done)
       if (x.n_rows - x.r0 <= t * kRows) return true;  // no such tile
       {
         uint8_t* qt = q_s + t * C::kTile;
         constexpr int cpr = D / 8;  // 16-byte runs of a row
-#pragma unroll 8
-        for (int i = threadIdx.x & 127; i < kRows * cpr; i += 128) {
-          const int rr = i / cpr, c = i % cpr, r = x.r0 + t * kRows + rr;
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (r < x.n_rows && !zero)
-            w = ldg_stream_u4(a.q + (int64_t)(x.sg.row0 + r / G) * a.ldq + (int64_t)(x.head * G + r % G) * D + 8 * c);
-          w.x ^= flip, w.y ^= flip, w.z ^= flip, w.w ^= flip;
-          *reinterpret_cast<uint4*>(qt + (c >> 3) * C::kHalf + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = w;
+        // a thread has one run of every 128 / cpr-th row; all its loads first
+        const int c = threadIdx.x & (cpr - 1), rr0 = (threadIdx.x & 127) / cpr;
+        const __half* qh = a.q + (int64_t)x.sg.row0 * a.ldq + (int64_t)x.head * G * D + 8 * c;
+        uint4 w[cpr];
+#pragma unroll
+        for (int i = 0; i < cpr; ++i) {
+          const int r = x.r0 + t * kRows + rr0 + i * (128 / cpr), tok = token_of(r);
+          w[i] = make_uint4(0, 0, 0, 0);
+          if (r < x.n_rows && !zero) w[i] = ldg_stream_u4(qh + (int64_t)tok * a.ldq + (r - tok * G) * D);
+        }
+#pragma unroll
+        for (int i = 0; i < cpr; ++i) {
+          const int rr = rr0 + i * (128 / cpr);
+          *reinterpret_cast<uint4*>(qt + (c >> 3) * C::kHalf + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) =
+              make_uint4(w[i].x ^ flip, w[i].y ^ flip, w[i].z ^ flip, w[i].w ^ flip);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
@@ -513,50 +516,6 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
       }
       __stcg(part + D * kRows, m);
       __stcg(part + (D + 1) * kRows, l);
-      __threadfence();
-      // the blocks that share the unit: from the one where it begins
-      int b0 = blockIdx.x, b1 = blockIdx.x;
-      while (sh.unit[b0] == u && sh.step[b0] > 0) --b0;
-      while (sh.unit[b1 + 1] == u && sh.step[b1 + 1] < x.n_steps) ++b1;
-      if (!all()) return false;
-      if (row == 0) {
-        uint32_t* cnt_p = a.arrivals + 2 * b0 + t;
-        const uint32_t prev = atomicAdd(cnt_p, 1u);
-        const bool last = (int)prev == b1 - b0;
-        if (last) *cnt_p = 0;  // for the next launch
-        tmem_slot[1 + t] = last;
-      }
-      if (!all()) return false;
-      if (!tmem_slot[1 + t]) return true;
-      __threadfence();
-      auto part_of = [&](int b) {
-        const int slot = 2 * b + (u == sh.unit[b] ? 0 : 1);
-        return a.part + (int64_t)(2 * slot + t) * kPart + row;
-      };
-      float mt = -INFINITY, lt = 0.f;
-#pragma unroll 4
-      for (int b = b0; b <= b1; ++b) mt = fmaxf(mt, __ldcg(part_of(b) + D * kRows));
-#pragma unroll 4
-      for (int b = b0; b <= b1; ++b) {
-        const float mb = __ldcg(part_of(b) + D * kRows);
-        lt = fmaf(mb == -INFINITY ? 0.f : ex2(mb - mt), __ldcg(part_of(b) + (D + 1) * kRows), lt);
-      }
-      const float inv = 1.0f / lt;
-#pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        float o[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = 0.f;
-#pragma unroll 2
-        for (int b = b0; b <= b1; ++b) {
-          const float* pb = part_of(b);
-          const float mb = __ldcg(pb + D * kRows);
-          const float f = mb == -INFINITY ? 0.f : ex2(mb - mt);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = fmaf(f, __ldcg(pb + (c + i) * kRows), o[i]);
-        }
-        store(c, o, inv);
-      }
       return true;
     });
   }
@@ -576,7 +535,8 @@ cudaError_t launch_tc_t(const Launch& L, const AttendArgs& a, const AttendShares
   if (e != cudaSuccess) return e;
   attend_tc_kernel<D, KV><<<sh.n, C::kThreads, C::kSmem, L.stream>>>(map, a, sh);
   if (L.counter) ++*L.counter;
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  return e == cudaSuccess ? launch_attend_merge(L, a, sh, 2, false) : e;
 }
 template <int D>
 cudaError_t launch_tc_kv(const Launch& L, const AttendArgs& a, const AttendShares& sh) {

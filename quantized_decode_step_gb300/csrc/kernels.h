@@ -319,10 +319,18 @@ __host__ __device__ inline int attend_unit_steps(int pos0, int n_rows, int G, in
 }
 void attend_shares(AttendArgs& a, int tile_rows, int step_keys, int max_blocks, int min_steps, int piece,
                    AttendShares& sh);
+// Units cut into parts: blocks first .. last, the first's part in slot `slot`, block b's in 2 b.
+struct AttendCuts {
+  int32_t n;
+  int32_t unit[kAttendMaxShares], first[kAttendMaxShares], last[kAttendMaxShares], slot[kAttendMaxShares];
+};
+// Puts the parts of cut units together, `tiles` tiles of 128 rows a unit; perm: the columns are in the order that the
+// streaming kernel leaves INT4 values in. No launch where no unit is cut.
+cudaError_t launch_attend_merge(const Launch& L, const AttendArgs& a, const AttendShares& sh, int tiles, bool perm);
 // Workspace: two cut pieces a block, of 16 rows of 128 values, or of two tiles of 128 rows of 128 values and (m, l).
 constexpr size_t kAttendPartFloats = (size_t)kAttendMaxShares * 2 * 2 * 130 * 128;
 constexpr size_t kAttendMlFloats = (size_t)kAttendMaxShares * 2 * 16 * 2;
-constexpr size_t kAttendArrivals = 2 * kAttendMaxShares;
+constexpr size_t kAttendArrivals = kAttendMaxShares;
 // Few rows: tiles of 8 or 16 rows.
 cudaError_t launch_attend_few(const Launch& L, AttendArgs& a, int n_sm, int tile_rows);
 // Up to 128 rows of many keys (tcgen05).
