@@ -7,6 +7,7 @@ fallback implementation.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import threading
@@ -114,6 +115,8 @@ def build(force: bool = False) -> str:
 def lib():
     """Load libmag.so (raises if it is missing: build it with ``build()``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -138,11 +141,11 @@ def lib():
                 "mag_verify_tokens": ([vp, i32, i32, vp, vp], i32),
                 "mag_prefill_batch": ([vp, i32, P32, P32, vp, vp], i32),
                 "mag_sync": ([vp], i32),
-                "mag_session_extend": ([vp, i32, P32, P32], i32),
-                "mag_kv_write": ([vp, i32, i32, P32, P32, vp, vp, i64], i32),
-                "mag_kv_read": ([vp, i32, i32, P32, P32, vp, vp, i64], i32),
+                "mag_session_extend": ([vp, i32, vp, vp], i32),
+                "mag_kv_write": ([vp, i32, i32, vp, vp, vp, vp, i64], i32),
+                "mag_kv_read": ([vp, i32, i32, vp, vp, vp, vp, i64], i32),
                 "mag_kv_export": ([vp, i32, i32, i32, vp, vp], i32),
-                "mag_attend": ([vp, i32, i32, P32, P32, vp, i64, vp, i64, i32, ctypes.c_float], i32),
+                "mag_attend": ([vp, i32, i32, vp, vp, vp, i64, vp, i64, i32, ctypes.c_float], i32),
                 "mag_sample": ([vp, i32, i32, i32, i64, ctypes.POINTER(SampleParams), vp, vp, vp, vp], i32),
                 "mag_get_memory_stats": ([vp, ctypes.POINTER(MemoryStats)], i32),
                 "mag_get_step_stats": ([vp, ctypes.POINTER(StepStats)], i32),
@@ -277,12 +280,17 @@ def hot_pool_blocks(p90, n_sessions, slack=1.2) -> int:
     return int(lib().mag_hot_pool_blocks(p90, n_sessions, slack))
 
 
-def _lists(sessions, n_tokens):
-    """(count, session ids, token counts) as the C calls take them."""
-    if len(sessions) != len(n_tokens):
-        raise ValueError(f"{len(sessions)} sessions but {len(n_tokens)} token counts")
-    n = len(sessions)
-    return n, (ctypes.c_int32 * n)(*sessions), (ctypes.c_int32 * n)(*n_tokens)
+class _Lists:
+    """Session ids and token counts as the C calls take them: one array of int32, the counts behind the ids."""
+
+    def __init__(self, sessions, n_tokens):
+        self.n = len(sessions)
+        if self.n != len(n_tokens):
+            raise ValueError(f"{self.n} sessions but {len(n_tokens)} token counts")
+        self.both = array.array("i", sessions)
+        self.both.extend(n_tokens)
+        self.ids = self.both.buffer_info()[0]
+        self.counts = self.ids + 4 * self.n
 
 
 class Context:
@@ -365,19 +373,20 @@ class Context:
 
     def session_extend(self, sessions, n_tokens):
         """Make room for n_tokens[i] new tokens of every session (written later, layer by layer)."""
-        self._check(lib().mag_session_extend(self.h, *_lists(sessions, n_tokens)), "mag_session_extend")
+        a = _Lists(sessions, n_tokens)
+        self._check(lib().mag_session_extend(self.h, a.n, a.ids, a.counts), "mag_session_extend")
 
     def kv_write(self, layer, sessions, n_tokens, k, v, ld=None):
         """Keys and values [rows, n_kv_heads, head_dim] of the sessions' newest tokens into one layer of the pool."""
         ld = self.cfg.n_kv_heads * self.cfg.head_dim if ld is None else ld
-        self._check(lib().mag_kv_write(self.h, layer, *_lists(sessions, n_tokens), _ptr(k), _ptr(v), ld),
-                    "mag_kv_write")
+        a = _Lists(sessions, n_tokens)
+        self._check(lib().mag_kv_write(self.h, layer, a.n, a.ids, a.counts, _ptr(k), _ptr(v), ld), "mag_kv_write")
 
     def kv_read(self, layer, sessions, n_tokens, k, v, ld=None):
         """The same rows back, as fp16."""
         ld = self.cfg.n_kv_heads * self.cfg.head_dim if ld is None else ld
-        self._check(lib().mag_kv_read(self.h, layer, *_lists(sessions, n_tokens), _ptr(k), _ptr(v), ld),
-                    "mag_kv_read")
+        a = _Lists(sessions, n_tokens)
+        self._check(lib().mag_kv_read(self.h, layer, a.n, a.ids, a.counts, _ptr(k), _ptr(v), ld), "mag_kv_read")
 
     def kv_export(self, sid, first, n_tokens, k, v):
         """Tokens first .. of one session in every layer, fp16 [n_layers, n_tokens, n_kv_heads, head_dim] each."""
@@ -388,7 +397,8 @@ class Context:
         the pool (scale: head_dim ** -0.5 by default)."""
         width = self.cfg.n_heads * self.cfg.head_dim
         scale = self.cfg.head_dim ** -0.5 if scale is None else scale
-        self._check(lib().mag_attend(self.h, layer, *_lists(sessions, n_tokens), _ptr(q), width if ldq is None else ldq,
+        a = _Lists(sessions, n_tokens)
+        self._check(lib().mag_attend(self.h, layer, a.n, a.ids, a.counts, _ptr(q), width if ldq is None else ldq,
                                      _ptr(out), width if ldo is None else ldo, window, scale), "mag_attend")
 
     def sync(self):

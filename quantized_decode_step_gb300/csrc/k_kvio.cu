@@ -32,88 +32,134 @@ __device__ __forceinline__ int block_of(const PoolGeom& P, int sess, int pos, ui
   return checked_block(P.tables[(int64_t)sess * P.table_stride + (pos >> 4)], (int)P.pool_blocks, err);
 }
 
-// Unit u of a row: 8 values, the units of the row's K heads first, then those of its V heads.
+// rint(x / s) of 8 values as clamp(.., lo, hi), as IEEE division and round-half-even decide it, without a division for
+// most: q = rint(x / s) from the reciprocal, and the remainder x - q s, which fp32 holds exactly, says how far the
+// quotient lies from halfway between two codes. Within 2^-17 of that (the reciprocal's quotient is off by at most 2^-18
+// for codes up to 15; up to 127, quotients of fp16 numbers are halfway or at least 2^-12 off) the division decides.
+// A scale below fp16's normal numbers is rounded coarsely: only then can a quotient pass the codes' range.
+__device__ __forceinline__ void codes8(const float (&x)[8], float s, int lo, int hi, int (&q)[8]) {
+  const float inv = s != 0.f ? 1.0f / s : 0.f;  // 0: every code 0
+  float close = INFINITY;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float m = fmaf(x[i], inv, 12582912.0f), r = fmaf(-(m - 12582912.0f), s, x[i]);
+    q[i] = __float_as_int(m) - 0x4B400000;
+    close = fminf(close, fabsf(fmaf(2.0f, fabsf(r), -s)));
+  }
+  if (s != 0.f && (close <= s * 1.52587890625e-5f || s < 6.103515625e-5f)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = max(lo, min(hi, (int)rintf(__fdiv_rn(x[i], s))));
+  }
+}
+
+// The stored form of 8 values of one vector, by the d / 8 neighbouring lanes that have it (e: which of them).
 template <int KV>
-__global__ void __launch_bounds__(kIoThreads) kv_write_kernel(const KvWriteArgs a) {
+__device__ __forceinline__ void store8(const PoolGeom& P, int layer, int blk, int part, int head, int slot, int e, int upv,
+                                       const uint4& w, bool live) {
+  uint8_t* data = pool_vec(P, layer, blk, part, head, slot);
+  if (KV == 0) {
+    if (live) reinterpret_cast<uint4*>(data)[e] = w;
+    return;
+  }
+  const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(u32_as_h2(ww[i]));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+  if (KV == 1) {
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
+    for (int o = upv >> 1; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const __half s16 = __float2half_rn(__fdiv_rn(amax, 127.0f));
+    const float sc = __half2float(s16);
+    int q[8];
+    codes8(x, sc, -127, 127, q);
+    uint32_t c[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i >> 2] |= (uint32_t)(q[i] & 255) << (8 * (i & 3));
+    if (live) {
+      reinterpret_cast<uint2*>(data)[e] = make_uint2(c[0], c[1]);
+      if (e == 0) *reinterpret_cast<__half*>(pool_vec(P, layer, blk, part + 2, head, slot)) = s16;
+    }
+  } else {
+    // minimum and maximum of the group's 4 lanes; of equal minima the first in index order (the sign of zero)
+    float lo = x[0], hi = x[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+      if (x[i] < lo) lo = x[i];
+      if (x[i] > hi) hi = x[i];
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      const float l2 = __shfl_xor_sync(0xffffffffu, lo, o), h2 = __shfl_xor_sync(0xffffffffu, hi, o);
+      const bool first = (threadIdx.x & o) == 0;
+      if (l2 < lo || (l2 == lo && !first)) lo = l2;
+      if (h2 > hi) hi = h2;
+    }
+    const __half s16 = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
+    const __half m16 = __float2half_rn(lo);
+    const float sc = __half2float(s16), mn = __half2float(m16);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __fsub_rn(x[i], mn);
+    int q[8];
+    codes8(x, sc, 0, 15, q);
+    uint32_t c = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c |= (uint32_t)q[i] << (4 * i);
+    if (live) {
+      reinterpret_cast<uint32_t*>(data)[e] = c;
+      if ((e & 3) == 0)
+        reinterpret_cast<__half2*>(pool_vec(P, layer, blk, part + 2, head, slot))[e >> 2] = __halves2half2(s16, m16);
+    }
+  }
+}
+
+// A block has NR neighbouring rows; unit u of a row: 8 values, the units of its K heads first, then those of its V
+// heads. A thread loads its unit of all NR rows before it stores the first.
+template <int KV, int NR>
+__global__ void __launch_bounds__(kIoThreads) kv_write_kernel(const __grid_constant__ KvWriteArgs a) {
   const PoolGeom& P = a.pool;
   const int d = P.head_dim, upv = d >> 3;                 // units per vector
   const int upr = 2 * P.n_kv_heads * upv;                 // units per row
-  const int row = blockIdx.x;
-  const int s = seg_of_row(a.rows, row);
-  const int pos = a.rows.seg[s].pos0 + row - a.rows.seg[s].row0;
-  const int blk = block_of(P, a.rows.seg[s].sess, pos, a.err);
-  // whole warps run to the end, so that the shuffles below have every lane (upv divides 32)
-  for (int u0 = threadIdx.x & ~31; u0 < upr; u0 += kIoThreads) {
+  const int row0 = blockIdx.x * NR;
+  __shared__ int s_blk[NR], s_slot[NR];
+  if (threadIdx.x < NR && row0 + threadIdx.x < a.rows.n_rows) {
+    const int row = row0 + threadIdx.x, s = seg_of_row(a.rows, row);
+    const int pos = a.rows.seg[s].pos0 + row - a.rows.seg[s].row0;
+    s_blk[threadIdx.x] = block_of(P, a.rows.seg[s].sess, pos, a.err);
+    s_slot[threadIdx.x] = pos & 15;
+  }
+  const int nr = min(NR, a.rows.n_rows - row0);
+  int part, head, e;
+  bool live;
+  uint4 w[NR];
+  auto load = [&](int u0) {  // of this lane's unit in the warp's units u0 .. u0 + 31
     const int u = u0 + (threadIdx.x & 31);
-    const bool live = u < upr;
-    const int vec = live ? u / upv : 0, e = live ? u - vec * upv : 0;
-    const int part = vec >= P.n_kv_heads, head = vec - part * P.n_kv_heads;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (live)
-      w = ldg_stream_u4((part ? a.v : a.k) + (int64_t)row * a.ld + head * d + 8 * e);
-    uint8_t* data = pool_vec(P, a.layer, blk, part, head, pos & 15);
-    if (KV == 0) {
-      if (live) reinterpret_cast<uint4*>(data)[e] = w;
-      continue;
+    live = u < upr;
+    const int vec = live ? u / upv : 0;
+    e = live ? u - vec * upv : 0;
+    part = vec >= P.n_kv_heads, head = vec - part * P.n_kv_heads;
+    const __half* src = (part ? a.v : a.k) + (int64_t)row0 * a.ld + head * d + 8 * e;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      w[r] = make_uint4(0, 0, 0, 0);
+      if (live && r < nr) w[r] = ldg_stream_u4(src + r * a.ld);
     }
-    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-    float x[8];
+  };
+  // whole warps run to the end, so that store8's shuffles have every lane (upv divides 32)
+  int u0 = threadIdx.x & ~31;
+  if (u0 < upr) load(u0);
+  __syncthreads();  // the rows' places
+  while (u0 < upr) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(u32_as_h2(ww[i]));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
-    if (KV == 1) {
-      float amax = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
-      for (int o = upv >> 1; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      const __half s16 = __float2half_rn(__fdiv_rn(amax, 127.0f));
-      const float sc = __half2float(s16);
-      uint32_t c[2] = {0, 0};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        int q = 0;
-        if (sc != 0.0f) q = max(-127, min(127, (int)rintf(__fdiv_rn(x[i], sc))));
-        c[i >> 2] |= (uint32_t)(q & 255) << (8 * (i & 3));
-      }
-      if (live) {
-        reinterpret_cast<uint2*>(data)[e] = make_uint2(c[0], c[1]);
-        if (e == 0) *reinterpret_cast<__half*>(pool_vec(P, a.layer, blk, part + 2, head, pos & 15)) = s16;
-      }
-    } else {
-      // minimum and maximum of the group's 4 lanes; of equal minima the first in index order (the sign of zero)
-      float lo = x[0], hi = x[0];
-#pragma unroll
-      for (int i = 1; i < 8; ++i) {
-        if (x[i] < lo) lo = x[i];
-        if (x[i] > hi) hi = x[i];
-      }
-#pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        const float l2 = __shfl_xor_sync(0xffffffffu, lo, o), h2 = __shfl_xor_sync(0xffffffffu, hi, o);
-        const bool first = (threadIdx.x & o) == 0;
-        if (l2 < lo || (l2 == lo && !first)) lo = l2;
-        if (h2 > hi) hi = h2;
-      }
-      const __half s16 = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
-      const __half m16 = __float2half_rn(lo);
-      const float sc = __half2float(s16), mn = __half2float(m16);
-      uint32_t c = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        int q = 0;
-        if (sc != 0.0f) q = max(0, min(15, (int)rintf(__fdiv_rn(__fsub_rn(x[i], mn), sc))));
-        c |= (uint32_t)q << (4 * i);
-      }
-      if (live) {
-        reinterpret_cast<uint32_t*>(data)[e] = c;
-        if ((e & 3) == 0)
-          reinterpret_cast<__half2*>(pool_vec(P, a.layer, blk, part + 2, head, pos & 15))[e >> 2] =
-              __halves2half2(s16, m16);
-      }
-    }
+    for (int r = 0; r < NR; ++r)
+      if (r < nr) store8<KV>(P, a.layer, s_blk[r], part, head, s_slot[r], e, upv, w[r], live);
+    u0 += kIoThreads;
+    if (u0 < upr) load(u0);
   }
 }
 
@@ -174,14 +220,21 @@ __global__ void __launch_bounds__(kIoThreads) kv_read_kernel(const KvReadArgs a)
 
 }  // namespace
 
+template <int KV>
+static cudaError_t launch_write_t(const Launch& L, const KvWriteArgs& a) {
+  // one row a block leaves no load waiting for another row's; of many rows, four a block keep more bytes in flight
+  // (7,000 rows of 8 heads, d 128, INT4: 12 us against 22)
+  const int n = a.rows.n_rows;
+  if (n <= 512) kv_write_kernel<KV, 1><<<n, kIoThreads, 0, L.stream>>>(a);
+  else kv_write_kernel<KV, 4><<<(n + 3) / 4, kIoThreads, 0, L.stream>>>(a);
+  if (L.counter) ++*L.counter;
+  return cudaGetLastError();
+}
+
 cudaError_t launch_kv_write(const Launch& L, const KvWriteArgs& a) {
   const int n = a.rows.n_rows;
   if (n < 1 || a.rows.n_seg < 1 || a.rows.n_seg > MAG_MAX_BATCH) return cudaErrorInvalidValue;
-  if (a.pool.kv_dtype == 0) kv_write_kernel<0><<<n, kIoThreads, 0, L.stream>>>(a);
-  else if (a.pool.kv_dtype == 1) kv_write_kernel<1><<<n, kIoThreads, 0, L.stream>>>(a);
-  else kv_write_kernel<2><<<n, kIoThreads, 0, L.stream>>>(a);
-  if (L.counter) ++*L.counter;
-  return cudaGetLastError();
+  return a.pool.kv_dtype == 0 ? launch_write_t<0>(L, a) : (a.pool.kv_dtype == 1 ? launch_write_t<1>(L, a) : launch_write_t<2>(L, a));
 }
 
 cudaError_t launch_kv_read(const Launch& L, const KvReadArgs& a, int n_layers) {

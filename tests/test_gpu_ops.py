@@ -93,6 +93,42 @@ def test_write_stores_the_bytes_of_append(kv, kv_heads, dim):
     assert na == nb and torch.equal(device_bytes(pa, na), device_bytes(pb, nb))
 
 
+@pytest.mark.parametrize("kv", [mag.KV_INT8, mag.KV_INT4], ids=KV_NAMES.get)
+def test_write_decides_codes_like_division(kv):
+    """Vectors made for quotients halfway between two codes, next to it, and of every magnitude down to fp16's smallest
+    number: what is read back equals the oracle's quantisers' to the bit."""
+    rng = np.random.default_rng(17)
+    n, h, d = 3000, 8, 128
+    x = rng.standard_normal((n, h, d)) * np.exp2(rng.integers(-24, 9, (n, h, 1)))
+    # the scale's own multiples and half multiples: integers and halves below a maximum of 127 (or 15 steps) times a power of two
+    unit = np.exp2(rng.integers(-10, 6, (n // 2, h, 1)))
+    top = 127 if kv == mag.KV_INT8 else 15
+    x[::2] = rng.integers(-2 * top, 2 * top + 1, (n // 2, h, d)) * 0.5 * unit
+    x[::2, :, ::32] = top * unit
+    if kv == mag.KV_INT4:
+        x[::2] = np.abs(x[::2])
+        x[::2, :, 1::32] = 0.0
+        x[1::4] += rng.standard_normal((len(x[1::4]), h, 1)) * 100
+    x = torch.from_numpy(np.clip(x, -60000, 60000).astype(np.float16))
+    x[5, 0] = 6e-8
+    x[7, 1, 3] = 6e-8
+    ctx = make(kv, heads=h, kv_heads=h, dim=d, pool_blocks=200, max_context=n + 16)
+    sid = ctx.session_open()
+    ctx.session_extend([sid], [n])
+    xd = x.cuda()
+    for step in (n, 100):  # as one call, and as calls of few rows
+        for at in range(0, n, step):
+            if step != n:
+                ctx.session_truncate(sid, at)
+                ctx.session_extend([sid], [step])
+            ctx.kv_write(0, [sid], [step], xd[at:at + step], xd[at:at + step])
+        out = torch.empty((2, n, h, d), dtype=torch.float16, device="cuda")
+        ctx.kv_read(0, [sid], [n], out[0], out[1])
+        ctx.sync()
+        want = as_stored(x, kv)
+        assert torch.equal(out[0].cpu(), want) and torch.equal(out[1].cpu(), want)
+
+
 @pytest.mark.parametrize("kv", ALL_KV, ids=KV_NAMES.get)
 @pytest.mark.parametrize("kv_heads,dim", [(1, 64), (3, 128), (8, 128)])
 def test_read_gives_the_stored_values(kv, kv_heads, dim):

@@ -41,4 +41,6 @@ def test_null_context(lib):
 
 def test_lists_of_unlike_length():
     with pytest.raises(ValueError):
-        mag._lists([1, 2], [3])
+        mag._Lists([1, 2], [3])
+    a = mag._Lists([5, 6], [7, 8])
+    assert a.n == 2 and list((ctypes.c_int32 * 4).from_address(a.ids)) == [5, 6, 7, 8] and a.counts == a.ids + 8
