@@ -1,19 +1,21 @@
-// Attention of the newest tokens of several sessions over one layer's block pool, for up to 128 packed rows and many
-// keys: tcgen05, one tile of rows, the keys in two streams.
+// Attention of the newest tokens of several sessions over one layer's block pool, for 17 to 128 packed rows: tcgen05, one
+// tile of rows, the keys in two streams.
 //
 //   o_t = sum_j softmax_j(scale q_t . k_j) v_j   over the keys j <= p_t, and j > p_t - window if there is one.
 //
-// What bounds it: K and V are read once for all rows, so with few rows the pool's bytes from HBM, and of INT8 and
-// INT4 pools the instructions that expand them. A 128-row MMA tile is mostly padding then, but the tensor core has the
-// time (2 x 512 clocks a step of 128 keys against 900 .. 2,800 for the step's bytes), and everything that costs
-// instructions is done once: the expansion by eight warps of their own (17 instructions for 8 INT4 values, where
-// the register kernel spends 44 with what lies around it), the softmax by the one warp per stream that has rows.
+// What bounds it: K and V are read once for all rows, so with one tile of rows the loads and the chain from a step's
+// scores to its products, about 1.5 us a step of 128 keys in each stream. A 128-row MMA tile is mostly padding with few rows,
+// but the tensor core has the time, and everything that costs instructions is done once: the expansion of INT8 and INT4
+// by eight warps of their own, the softmax by the one warp per stream and 32 rows that has any. 20 rows over 20,000
+// FP16 keys, 8 KV heads of 128: 68 us in 16-row tiles of the register kernel, 30 here; 128 rows of INT4 80 against 34. For up
+// to 16 rows the register kernel reads the keys once as well and is faster (16 rows over 16 sessions' INT8 keys 59 us
+// against 156).
 //
 // Even and odd steps of 128 keys are two streams with a maximum, a sum and an o each, so that one's softmax runs while
-// the tensor core has the other's products; they are joined at the end, in tensor memory. Roles, rings, the
-// softmax's base and lazy maximum and the equal shares of all units' steps are those of k_attend_tc.cu; the sum adds
-// the rounded p, as the register kernel does. INT4 values are left in the order that their expansion makes them in
-// (0, 4, 1, 5, 2, 6, 3, 7 of every eight): of K it only has to be Q's, of V it is undone as o is stored.
+// the tensor core has the other's products; they are joined at the end, in tensor memory. Roles, the softmax's base and
+// lazy maximum and the shares of the units' steps are those of k_attend_tc.cu; the sum adds the rounded p, as the register
+// kernel does. INT4 values are left in the order that their expansion makes them in (0, 4, 1, 5, 2, 6, 3, 7 of every
+// eight): of K it only has to be Q's, of V it is undone as o is stored.
 #include <algorithm>
 
 #include "attend_tc.cuh"
@@ -24,27 +26,248 @@ namespace {
 
 using namespace tc;
 
+// The ring of K and V tiles (fp16, 128 keys, 128-byte swizzled halves of 64 dimensions) in shared memory.
+// FP16: a loader warp fills it by TMA. INT8, INT4: kExpand warps copy the stored bytes into slots of their own, kRaw
+// tiles ahead, each thread the 16-byte runs that it expands later, so that no thread waits for another's copies
+// (128 rows over 20,000 INT4 keys: 33.6 us; 37.5 with a loader warp that issues a bulk copy per pool block). Tiles come and
+// go in the order of in_order().
 template <int D, int KV>
-struct Cfg {
+struct RingShape {
   static constexpr int kTile = kKeys * D * 2, kHalf = kKeys * 128;
   static constexpr int kStages = D == 128 ? (KV == 0 ? 6 : 4) : 8;
   static constexpr int kRowB = KV == 0 ? 2 * D : (KV == 1 ? D : D / 2), kMetaB = KV == 0 ? 0 : (KV == 1 ? 2 : D / 8);
-  static constexpr int kRawData = kKeys * kRowB, kRawMeta = kKeys * kMetaB;
-  static constexpr int kRaw = KV == 0 ? 0 : (KV == 1 ? 3 : 5);  // slots of raw bytes
-  static constexpr int kRawBytes = KV == 0 ? 0 : kRawData + kRawMeta;
-  static constexpr int kExpand = KV == 0 ? 0 : 8;               // expanding warps
+  static constexpr int kExpand = KV == 0 ? 0 : 8;  // expanding warps
+  static constexpr int kRuns = kRowB / 16;         // 16-byte runs of a stored row
+  static constexpr int kItems = KV == 0 ? 1 : kKeys * kRuns / (32 * 8);  // runs of a thread and tile
+  static constexpr int kRawBytes = KV == 0 ? 0 : kItems * 256 * 20;      // of a tile: a run and 4 bytes of its metadata each
+  static constexpr int kRaw = KV == 0 ? 0 : (kItems == 4 ? 3 : 6);
   static constexpr int kThreads = (12 + kExpand) * 32;
-  static constexpr int kBars = 2 * kStages + 2 * kRaw + 9;
-  static constexpr int kSmem = kTile + kStages * kTile + kRaw * kRawBytes + kRows * 8 + kBars * 8 + 64 + 1024;
+  static constexpr int kBytes = kStages * kTile + kRaw * kRawBytes, kBars = 2 * kStages;
+};
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {  // zeros where it is not
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
+}
+
+// The order in which a piece's tiles are loaded, expanded and used: K 0, K 1, then V j, K j + 2 for every step j.
+// f(step, part) with part 0 for K.
+template <typename F>
+__device__ __forceinline__ bool in_order(int s0, int s1, F f) {
+  if (!f(s0, 0)) return false;
+  if (s0 + 1 < s1 && !f(s0 + 1, 0)) return false;
+  for (int s = s0; s < s1; ++s) {
+    if (!f(s, 1)) return false;
+    if (s + 2 < s1 && !f(s + 2, 0)) return false;
+  }
+  return true;
+}
+
+template <int D, int KV>
+struct Ring : RingShape<D, KV> {
+  using S = RingShape<D, KV>;
+  uint8_t *tiles, *raw;
+  uint64_t *full, *empty;
+  __device__ Ring(uint8_t* mem, uint64_t* bars)
+      : tiles(mem), raw(mem + S::kStages * S::kTile), full(bars), empty(full + S::kStages) {}
+  __device__ void init() const {
+    for (int i = 0; i < S::kStages; ++i) {
+      mb_init(full + i, KV == 0 ? 1 : S::kExpand);
+      mb_init(empty + i, 1);
+    }
+  }
+
+  // FP16's loader warp: share(f) calls f(session, head, first key, first step, end step) for every piece.
+  template <typename Share>
+  __device__ void load(const CUtensorMap& map, const AttendArgs& a, Share share) const {
+    const int lane = threadIdx.x & 31;
+    const PoolGeom& P = a.pool;
+    const uint8_t* layer_base = P.base + (int64_t)a.layer * P.pool_blocks * P.block_bytes;
+    const int64_t data_part = (int64_t)P.n_kv_heads * 16 * S::kRowB;
+    int g = 0;
+    share([&](const AttendSeg& sg, int head, int key0, int s0, int s1) {
+      const int32_t* table = P.tables + (int64_t)sg.sess * P.table_stride;
+      const int len = sg.pos0 + sg.n_tok, n_blk = (len + 15) >> 4;
+      // block ids, one a lane: of four steps from `at` on; V comes two steps after K, so two such windows
+      int ids[2] = {0, 0}, at[2] = {-4, -4};
+      return in_order(s0, s1, [&](int s, int part) {
+        const int key = key0 + s * kKeys, b0 = key >> 4;
+        if (s >= at[part] + 4 || at[part] < s0) {
+          const int b = b0 + lane;
+          ids[part] = b < n_blk ? checked_block(table[b], (int)P.pool_blocks, a.err) : 0;
+          at[part] = s;
+        }
+        const int nb = min(8, n_blk - b0);        // pool blocks of this step
+        const int nv = min(8, (len - key) >> 4);  // of them, whole ones
+        const int id_w = ids[part], id_at = (s - at[part]) * 8;
+        const int my = __shfl_sync(0xffffffffu, id_w, id_at + (lane & 7));
+        const int st = g % S::kStages;
+        if (g >= S::kStages && !mb_wait(empty + st, ((g / S::kStages) - 1) & 1)) {
+          if (lane == 0) atomicOr(a.err, kErrAttend);
+          return false;
+        }
+        uint8_t* tile = tiles + st * S::kTile;
+        int n_tma = nb;
+        if (part == 1 && nv < 8) {
+          // the step that holds the session's end: value rows past it are zeros (a slot there may hold anything, and 0
+          // times it must be 0), the block it lies in is copied row by row
+          n_tma = nv;
+          const int y0 = nv * 16;
+          for (int i = lane; i < (kKeys - y0) * (D / 8); i += 32) {  // a multiple of 32
+            const int row = y0 + i / (D / 8), c = i % (D / 8);
+            uint4 w = make_uint4(0, 0, 0, 0);
+            const int b = __shfl_sync(0xffffffffu, id_w, id_at + (row >> 4));
+            if (key + row < len)
+              w = *reinterpret_cast<const uint4*>(layer_base + (int64_t)b * P.block_bytes + data_part +
+                                                  ((int64_t)head * 16 + (row & 15)) * S::kRowB + 16 * c);
+            *reinterpret_cast<uint4*>(tile + (c >> 3) * S::kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = w;
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
+        if (lane == 0) mb_expect(full + st, (uint32_t)n_tma * 16 * D * 2);
+        __syncwarp();
+        const int blk = lane & 7, half = lane >> 3;
+        if (blk < n_tma && half < D / 64)
+          tma_2d(su32(tile) + half * S::kHalf + blk * 2048, &map, half * 64, ((my * 2 + part) * P.n_kv_heads + head) * 16,
+                 full + st);
+        ++g;
+        return true;
+      });
+    });
+    // leave no copy in flight, also when a consumer gave up and will not wait for it
+    for (int f = max(0, g - S::kStages); f < g; ++f) mb_wait(full + f % S::kStages, (f / S::kStages) & 1);
+  }
+
+  // Expanding warp w of kExpand: copies tile g, then expands the one kRaw - 1 before it.
+  template <typename Share>
+  __device__ void expand(int w, const AttendArgs& a, Share share) const {
+    const int lane = threadIdx.x & 31, thread = w * 32 + lane;
+    const PoolGeom& P = a.pool;
+    const int64_t data_part = (int64_t)P.n_kv_heads * 16 * S::kRowB, meta_part = (int64_t)P.n_kv_heads * 16 * S::kMetaB;
+    // A warp's 32 runs are whole stored rows. Of 8 lanes side by side each writes another 16 bytes of the 128-byte
+    // swizzled rows: with two (INT8) or four (INT4) fp16 runs a lane that takes two rows, or four.
+    constexpr int kRq = KV == 1 ? 2 : 4, kRunQ = 8 / kRq, kQr = S::kRuns / kRunQ, kRowsW = 32 / S::kRuns;
+    const int run = (lane / kRq) % kRunQ + kRunQ * ((lane >> 3) % kQr);
+    const int row_w = (lane & (kRq - 1)) + kRq * ((lane >> 3) / kQr) + w * kRowsW;  // of item 0; 8 kRowsW further an item
+    const uint8_t* src0 = P.base + (int64_t)a.layer * P.pool_blocks * P.block_bytes;
+    const uint8_t* data0 = src0 + (row_w & 15) * S::kRowB + 16 * run;
+    const uint8_t* meta0 = src0 + 2 * data_part + (KV == 1 ? (row_w & 14) * 2 : (row_w & 15) * S::kMetaB + 4 * run);
+    const uint32_t raw16 = su32(raw) + thread * 16, raw4 = su32(raw) + S::kItems * 256 * 16 + thread * 4;
+    int g = 0;   // tiles copied
+    int ge = 0;  // and expanded
+    auto expand_next = [&] {
+      const int st = ge % S::kStages, r = ge % S::kRaw;
+      if (ge >= S::kStages && !mb_wait(empty + st, ((ge / S::kStages) - 1) & 1)) {
+        if (lane == 0) atomicOr(a.err, kErrAttend);
+        return false;
+      }
+      const uint8_t* src = raw + r * S::kRawBytes;
+#pragma unroll
+      for (int i = 0; i < S::kItems; ++i) {
+        const int row = row_w + i * 8 * kRowsW;
+        const uint4 c = *reinterpret_cast<const uint4*>(src + (i * 256 + thread) * 16);
+        uint32_t meta = *reinterpret_cast<const uint32_t*>(src + S::kItems * 256 * 16 + (i * 256 + thread) * 4);
+        if (KV == 1 && (row & 1)) meta >>= 16;
+        const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+        const __half2 sc = __low2half2(u32_as_h2(meta)), mn = __high2half2(u32_as_h2(meta));
+        uint8_t* row_p = tiles + st * S::kTile + row * 128;
+        if constexpr (KV == 1) {  // 16 values: two runs of 8
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t h = __byte_perm(cw[2 * e + (k >> 1)] ^ 0x80808080u, 0x64646464u, (k & 1) ? 0x4342 : 0x4140);
+              v[k] = h2_as_u32(__hmul2(__hsub2(u32_as_h2(h), u32_as_h2(0x64806480u)), sc));
+            }
+            const int cc = 2 * run + e;
+            *reinterpret_cast<uint4*>(row_p + (cc >> 3) * S::kHalf + (((cc & 7) ^ (row & 7)) << 4)) =
+                make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        } else {  // 32 values: four runs of 8, pairs (i, i + 4)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              v[k] = h2_as_u32(__hfma2(
+                  __hsub2(u32_as_h2(((cw[e] >> (4 * k)) & 0x000F000Fu) | 0x64006400u), u32_as_h2(0x64006400u)), sc, mn));
+            const int cc = 4 * run + e;
+            *reinterpret_cast<uint4*>(row_p + (cc >> 3) * S::kHalf + (((cc & 7) ^ (row & 7)) << 4)) =
+                make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mb_arrive(full + st);
+      ++ge;
+      return true;
+    };
+    bool ok = true;
+    share([&](const AttendSeg& sg, int head, int key0, int s0, int s1) {
+      const int32_t* table = P.tables + (int64_t)sg.sess * P.table_stride;
+      const int len = sg.pos0 + sg.n_tok, n_blk = (len + 15) >> 4;
+      // block ids, one a lane: of four steps from `at` on, and of the next four; V comes two steps after K
+      auto ids_at = [&](int s) {
+        const int b = ((key0 + s * kKeys) >> 4) + lane;
+        return b < n_blk ? table[b] : 0;
+      };
+      int ids[2], next[2], at[2] = {s0, s0};
+      ids[0] = ids[1] = checked_block(ids_at(s0), (int)P.pool_blocks, a.err);
+      next[0] = next[1] = ids_at(s0 + 4);
+      const uint8_t* data_h = data0 + (int64_t)head * 16 * S::kRowB;
+      const uint8_t* meta_h = meta0 + (int64_t)head * 16 * S::kMetaB;
+      ok = in_order(s0, s1, [&](int s, int part) {
+        if (s >= at[part] + 4) {
+          ids[part] = checked_block(next[part], (int)P.pool_blocks, a.err);
+          next[part] = ids_at(s + 4);
+          at[part] = s;
+        }
+        const int live = len - (key0 + s * kKeys);  // rows that hold tokens; the others become zeros
+        const uint32_t slot = (uint32_t)(g % S::kRaw) * S::kRawBytes;
+        const int my_ids = ids[part], id_at = (s - at[part]) * 8;
+#pragma unroll
+        for (int i = 0; i < S::kItems; ++i) {
+          const int row = row_w + i * 8 * kRowsW;
+          const int64_t blk = (int64_t)__shfl_sync(0xffffffffu, my_ids, id_at + (row >> 4)) * P.block_bytes;
+          copy16(raw16 + slot + i * 256 * 16, data_h + blk + part * data_part, row < live);
+          copy4(raw4 + slot + i * 256 * 4, meta_h + blk + part * meta_part, row < live);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (++g < S::kRaw) return true;
+        asm volatile("cp.async.wait_group %0;" ::"n"(S::kRaw - 1) : "memory");
+        return expand_next();
+      });
+      return ok;
+    });
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    while (ok && ge < g) ok = expand_next();
+  }
 };
 
+// Dimension of column c (of o, of a value row): INT4 leaves every eight in its expansion's order.
+template <int KV>
+__device__ __forceinline__ constexpr int dim_of(int c) {
+  return KV == 2 ? (c & ~7) | ((c & 1) * 4 + ((c & 7) >> 1)) : c;
+}
+// 8 fp16 values in that order.
+template <int KV>
+__device__ __forceinline__ uint4 in_expansion_order(const uint4& w) {
+  return KV == 2 ? make_uint4(__byte_perm(w.x, w.z, 0x5410), __byte_perm(w.x, w.z, 0x7632), __byte_perm(w.y, w.w, 0x5410),
+                              __byte_perm(w.y, w.w, 0x7632))
+                 : w;
+}
+
+// One tile of up to 128 packed rows of a session and KV head over its keys.
 struct Unit {
   AttendSeg sg;
   int head, r0, n_rows, live;  // first packed row, rows of the session, rows of the tile
   int p_lo, p_hi, key0, n_steps;
 };
-
-__device__ __forceinline__ Unit unit_at(const AttendArgs& a, int u) {
+__device__ __forceinline__ Unit unit_of(const AttendArgs& a, int u) {
   Unit x;
   int si = 0;
   for (int i = 1; i < a.n_seg; ++i)
@@ -64,29 +287,21 @@ __device__ __forceinline__ void for_share(const AttendArgs& a, const AttendShare
   int u = sh.unit[blockIdx.x], s = sh.step[blockIdx.x];
   const int ue = sh.unit[blockIdx.x + 1], se = sh.step[blockIdx.x + 1];
   while (u < ue || (u == ue && s < se)) {
-    const Unit x = unit_at(a, u);
+    const Unit x = unit_of(a, u);
     if (!f(x, u, s, u == ue ? se : x.n_steps)) return;
     ++u;
     s = 0;
   }
 }
-// The order in which a piece's tiles are loaded, expanded and used: K 0, K 1, then V j, K j + 2 for every step j.
-// f(step, part) with part 0 for K.
-template <typename F>
-__device__ __forceinline__ bool in_order(int s0, int s1, F f) {
-  if (!f(s0, 0)) return false;
-  if (s0 + 1 < s1 && !f(s0 + 1, 0)) return false;
-  for (int s = s0; s < s1; ++s) {
-    if (!f(s, 1)) return false;
-    if (s + 2 < s1 && !f(s + 2, 0)) return false;
-  }
-  return true;
-}
-// Dimension of column c (of o, of a value row): INT4 leaves every eight in its expansion's order.
-template <int KV>
-__device__ __forceinline__ constexpr int dim_of(int c) {
-  return KV == 2 ? (c & ~7) | ((c & 1) * 4 + ((c & 7) >> 1)) : c;
-}
+
+
+template <int D, int KV>
+struct Cfg : RingShape<D, KV> {
+  using R = RingShape<D, KV>;
+  static constexpr int kBars = R::kBars + 9;
+  static constexpr int kSmem = R::kTile + R::kBytes + kRows * 8 + kBars * 8 + 64 + 1024;
+};
+
 // 8 columns as fp16 in the order of their dimensions.
 template <int KV>
 __device__ __forceinline__ uint4 pack8(const float (&o)[8]) {
@@ -102,20 +317,15 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
     attend_stream_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ AttendArgs a,
                          const __grid_constant__ AttendShares sh) {
   using C = Cfg<D, KV>;
-  constexpr int ST = C::kStages, RAW = C::kRaw;
   constexpr uint32_t kIdescQK = (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
   constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_s = smem;
-  uint8_t* ring = smem + C::kTile;             // [ST][128 keys x D]
-  uint8_t* raw = ring + ST * C::kTile;         // [RAW] stored bytes: data, then scales
-  float2* ml_b = reinterpret_cast<float2*>(raw + RAW * C::kRawBytes);  // the second stream's (m, l)
-  uint64_t* full = reinterpret_cast<uint64_t*>(ml_b + kRows);
-  uint64_t* empty = full + ST;
-  uint64_t* raw_full = empty + ST;
-  uint64_t* raw_empty = raw_full + RAW;
-  uint64_t* q_full = raw_empty + RAW;
+  float2* ml_b = reinterpret_cast<float2*>(smem + C::kTile + C::kBytes);  // the second stream's (m, l)
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ml_b + kRows);
+  const Ring<D, KV> ring(smem + C::kTile, bars);
+  uint64_t* q_full = bars + C::R::kBars;
   uint64_t* s_full = q_full + 1;   // [2]: S of the stream is in tensor memory (and o holds its earlier steps)
   uint64_t* p_full = s_full + 2;   // [2]: P is
   uint64_t* o_full = p_full + 2;   // [2]: o is final
@@ -123,17 +333,8 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
   uint64_t* mma_done = joined + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const PoolGeom& P = a.pool;
-
   if (threadIdx.x == 0) {
-    for (int i = 0; i < ST; ++i) {
-      mb_init(full + i, KV == 0 ? 1 : C::kExpand);
-      mb_init(empty + i, 1);
-    }
-    for (int i = 0; i < RAW; ++i) {
-      mb_init(raw_full + i, 1);
-      mb_init(raw_empty + i, C::kExpand);
-    }
+    ring.init();
     mb_init(q_full, 8);
     for (int i = 0; i < 2; ++i) {
       mb_init(s_full + i, 1);
@@ -156,98 +357,20 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
 
   pdl_trigger();  // the merge kernel may be put in place; it waits for this grid's end
   if (warp == 0) {
-    // ---- loader
-    const uint8_t* layer_base = P.base + (int64_t)a.layer * P.pool_blocks * P.block_bytes;
-    const int64_t data_part = (int64_t)P.n_kv_heads * 16 * C::kRowB, meta_part = (int64_t)P.n_kv_heads * 16 * C::kMetaB;
-    int g = 0;
-    for_share(a, sh, [&](const Unit& x, int, int s0, int s1) {
-      const int32_t* table = P.tables + (int64_t)x.sg.sess * P.table_stride;
-      const int len = x.sg.pos0 + x.sg.n_tok, n_blk = (len + 15) >> 4;
-      // block ids, one a lane: of four steps from `at` on; V comes two steps after K, so two such windows
-      int ids[2] = {0, 0}, at[2] = {-4, -4};
-      return in_order(s0, s1, [&](int s, int part) {
-        const int key = x.key0 + s * kKeys, b0 = key >> 4;
-        if (s >= at[part] + 4 || at[part] < s0) {
-          const int b = b0 + lane;
-          ids[part] = b < n_blk ? checked_block(table[b], (int)P.pool_blocks, a.err) : 0;
-          at[part] = s;
-        }
-        const int nb = min(8, n_blk - b0);        // pool blocks of this step
-        const int nv = min(8, (len - key) >> 4);  // of them, whole ones
-        const int id_w = ids[part], id_at = (s - at[part]) * 8;
-        const int my = __shfl_sync(0xffffffffu, id_w, id_at + (lane & 7));
-        if constexpr (KV == 0) {
-          const int st = g % ST;
-          if (g >= ST && !mb_wait(empty + st, ((g / ST) - 1) & 1)) {
-            if (lane == 0) atomicOr(a.err, kErrAttend);
-            return false;
-          }
-          const uint32_t dst = su32(ring + st * C::kTile);
-          int n_tma = nb;
-          if (part == 1 && nv < 8) {
-            // the step that holds the session's end: value rows past it are zeros (a slot there may hold anything, and 0
-            // times it must be 0), the block it lies in is copied row by row
-            n_tma = nv;
-            const int y0 = nv * 16;
-            for (int i = lane; i < (kKeys - y0) * (D / 8); i += 32) {  // a multiple of 32
-              const int row = y0 + i / (D / 8), c = i % (D / 8);
-              uint4 w = make_uint4(0, 0, 0, 0);
-              const int b = __shfl_sync(0xffffffffu, id_w, id_at + (row >> 4));
-              if (key + row < len)
-                w = *reinterpret_cast<const uint4*>(layer_base + (int64_t)b * P.block_bytes + data_part +
-                                                    ((int64_t)x.head * 16 + (row & 15)) * C::kRowB + 16 * c);
-              *reinterpret_cast<uint4*>(ring + st * C::kTile + (c >> 3) * C::kHalf + row * 128 +
-                                        (((c & 7) ^ (row & 7)) << 4)) = w;
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-          }
-          if (lane == 0) mb_expect(full + st, (uint32_t)n_tma * 16 * D * 2);
-          __syncwarp();
-          const int blk = lane & 7, half = lane >> 3;
-          if (blk < n_tma && half < D / 64)
-            tma_2d(dst + half * C::kHalf + blk * 2048, &map, half * 64, ((my * 2 + part) * P.n_kv_heads + x.head) * 16,
-                   full + st);
-        } else {
-          const int r = g % RAW;
-          if (g >= RAW && !mb_wait(raw_empty + r, ((g / RAW) - 1) & 1)) {
-            if (lane == 0) atomicOr(a.err, kErrAttend);
-            return false;
-          }
-          const uint32_t dst = su32(raw + r * C::kRawBytes);
-          if (lane == 0) mb_expect(raw_full + r, (uint32_t)nb * 16 * (C::kRowB + C::kMetaB));
-          __syncwarp();
-          const int blk = lane & 7;
-          const uint8_t* base = layer_base + (int64_t)my * P.block_bytes;
-          if (lane < nb)
-            bulk_g2s(dst + blk * 16 * C::kRowB, base + part * data_part + (int64_t)x.head * 16 * C::kRowB, 16 * C::kRowB,
-                     raw_full + r);
-          else if (lane >= 8 && lane < 8 + nb)
-            bulk_g2s(dst + C::kRawData + blk * 16 * C::kMetaB,
-                     base + 2 * data_part + part * meta_part + (int64_t)x.head * 16 * C::kMetaB, 16 * C::kMetaB,
-                     raw_full + r);
-        }
-        ++g;
-        return true;
-      });
+    if constexpr (KV == 0) ring.load(map, a, [&](auto f) {
+      for_share(a, sh, [&](const Unit& x, int, int s0, int s1) { return f(x.sg, x.head, x.key0, s0, s1); });
     });
-    // leave no copy in flight, also when a consumer gave up and will not wait for it
-    if constexpr (KV == 0) {
-      for (int f = max(0, g - ST); f < g; ++f) mb_wait(full + f % ST, (f / ST) & 1);
-    } else {
-      for (int f = max(0, g - RAW); f < g; ++f) mb_wait(raw_full + f % RAW, (f / RAW) & 1);
-    }
   } else if (warp == 1) {
     if (lane == 0) {
       // ---- MMA issuer
       int g = 0, piece = 0, cnt[2] = {0, 0};
-      const uint32_t q_a = su32(q_s), ring_a = su32(ring);
+      const uint32_t q_a = su32(q_s), ring_a = su32(ring.tiles);
       for_share(a, sh, [&](const Unit&, int, int s0, int s1) {
         bool ok = mb_wait(q_full, piece & 1);
         ++piece;
         ok = ok && in_order(s0, s1, [&](int s, int part) {
-          const int t = (s - s0) & 1, st = g % ST;
-          if (!mb_wait(full + st, (g / ST) & 1)) return false;
+          const int t = (s - s0) & 1, st = g % C::kStages;
+          if (!mb_wait(ring.full + st, (g / C::kStages) & 1)) return false;
           if (part == 0) {
             tc_after();
             const uint64_t qd = smem_desc(q_a, 16), kd = smem_desc(ring_a + st * C::kTile, 16);
@@ -268,7 +391,7 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
                      (s - s0 > 1) || k != 0);
             if (s + 2 >= s1) mma_commit(o_full + t);
           }
-          mma_commit(empty + st);
+          mma_commit(ring.empty + st);
           ++g;
           return true;
         });
@@ -280,78 +403,10 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
       mb_wait(mma_done, 0);
     }
   } else if (warp >= 12) {
-    // ---- expansion of INT8 / INT4 tiles
-    if constexpr (KV != 0) {
-      const int w = warp - 12;
-      int g = 0;
-      for_share(a, sh, [&](const Unit& x, int, int s0, int s1) {
-        const int len = x.sg.pos0 + x.sg.n_tok;
-        return in_order(s0, s1, [&](int s, int) {
-          const int live = len - (x.key0 + s * kKeys);  // rows that hold tokens
-          const int r = g % RAW, st = g % ST;
-          if (!mb_wait(raw_full + r, (g / RAW) & 1) || (g >= ST && !mb_wait(empty + st, ((g / ST) - 1) & 1))) {
-            if (lane == 0) atomicOr(a.err, kErrAttend);
-            return false;
-          }
-          const uint8_t* src = raw + r * C::kRawBytes;
-          uint8_t* dst = ring + st * C::kTile;
-          // 16 stored bytes of one row a thread: 8 lanes side by side have 8 rows, whose 16-byte runs of a swizzled tile
-          // lie in different banks
-          constexpr int kRuns = C::kRowB / 16;              // of a row
-          constexpr int kItems = kKeys * kRuns / (32 * C::kExpand);
-          static_assert(kKeys * kRuns % (32 * C::kExpand) == 0, "expansion");
-#pragma unroll
-          for (int i = 0; i < kItems; ++i) {
-            const int item = (i * C::kExpand + w) * 32 + lane;
-            const int row = (item & 7) | ((item / (8 * kRuns)) << 3), run = (item >> 3) % kRuns;
-            uint4 c = make_uint4(0, 0, 0, 0);
-            uint32_t meta = 0;
-            if (row < live) {
-              c = *reinterpret_cast<const uint4*>(src + row * C::kRowB + 16 * run);
-              const uint8_t* mp = src + C::kRawData + row * C::kMetaB;
-              meta = KV == 1 ? *reinterpret_cast<const uint16_t*>(mp) : reinterpret_cast<const uint32_t*>(mp)[run];
-            }
-            const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
-            const __half2 sc = __low2half2(u32_as_h2(meta)), mn = __high2half2(u32_as_h2(meta));
-            uint8_t* row_p = dst + row * 128;
-            if constexpr (KV == 1) {  // 16 values: two runs of 8
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                uint32_t v[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const uint32_t h = __byte_perm(cw[2 * e + (k >> 1)] ^ 0x80808080u, 0x64646464u, (k & 1) ? 0x4342 : 0x4140);
-                  v[k] = h2_as_u32(__hmul2(__hsub2(u32_as_h2(h), u32_as_h2(0x64806480u)), sc));
-                }
-                const int cc = 2 * run + e;
-                *reinterpret_cast<uint4*>(row_p + (cc >> 3) * C::kHalf + (((cc & 7) ^ (row & 7)) << 4)) =
-                    make_uint4(v[0], v[1], v[2], v[3]);
-              }
-            } else {  // 32 values: four runs of 8, pairs (i, i + 4)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint32_t v[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  v[k] = h2_as_u32(__hfma2(
-                      __hsub2(u32_as_h2(((cw[e] >> (4 * k)) & 0x000F000Fu) | 0x64006400u), u32_as_h2(0x64006400u)), sc, mn));
-                const int cc = 4 * run + e;
-                *reinterpret_cast<uint4*>(row_p + (cc >> 3) * C::kHalf + (((cc & 7) ^ (row & 7)) << 4)) =
-                    make_uint4(v[0], v[1], v[2], v[3]);
-              }
-            }
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) {
-            mb_arrive(raw_empty + r);
-            mb_arrive(full + st);
-          }
-          ++g;
-          return true;
-        });
+    if constexpr (KV != 0)
+      ring.expand(warp - 12, a, [&](auto f) {
+        for_share(a, sh, [&](const Unit& x, int, int s0, int s1) { return f(x.sg, x.head, x.key0, s0, s1); });
       });
-    }
   } else if (warp >= 4) {
     // ---- softmax of stream t, one row a thread
     const int t = (warp >> 2) - 1, row = threadIdx.x & 127, wg = threadIdx.x - 128;  // wg: 0 .. 255 over both streams
@@ -381,9 +436,7 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
         uint4 w = make_uint4(0, 0, 0, 0);
         if (r < x.n_rows && !zero) w = ldg_stream_u4(qh + (int64_t)tok * a.ldq + (r - tok * G) * D);
         w.x ^= flip, w.y ^= flip, w.z ^= flip, w.w ^= flip;
-        if (KV == 2)
-          w = make_uint4(__byte_perm(w.x, w.z, 0x5410), __byte_perm(w.x, w.z, 0x7632), __byte_perm(w.y, w.w, 0x5410),
-                         __byte_perm(w.y, w.w, 0x7632));
+        w = in_expansion_order<KV>(w);
         *reinterpret_cast<uint4*>(q_s + (c >> 3) * C::kHalf + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = w;
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

@@ -333,7 +333,7 @@ constexpr size_t kAttendMlFloats = (size_t)kAttendMaxShares * 2 * 16 * 2;
 constexpr size_t kAttendArrivals = kAttendMaxShares;
 // Few rows: tiles of 8 or 16 rows.
 cudaError_t launch_attend_few(const Launch& L, AttendArgs& a, int n_sm, int tile_rows);
-// Up to 128 rows of many keys (tcgen05).
+// Up to 128 rows (tcgen05).
 cudaError_t launch_attend_stream(const Launch& L, AttendArgs& a, int n_sm);
 // Many rows (tcgen05); false where the pool is too large for it.
 bool attend_tc_fits(const AttendArgs& a);

@@ -87,10 +87,10 @@ static mag_status attend_workspace(mag_ctx* c) {
 }
 
 // Which kernel a session goes to, by its packed rows (tokens times query heads per KV head): up to kFewRows to the
-// register kernel, up to 128 (one tile) to the streaming one, others to the two-tile one. Of many keys the streaming
-// kernel is faster with few rows as well.
+// register kernel (one of its tiles; with the streaming kernel 16 sessions' single tokens over INT8 keys take 156 us for
+// 59), up to kStreamRows (one tile) to the streaming one (20 rows over 20,000 FP16 keys: 30 us for the register
+// kernel's 68), others to the two-tile one. A pool too large for a tensor map's rows goes to the register kernel whole.
 constexpr int kFewRows = 16, kStreamRows = 128;
-constexpr int64_t kFewBlocks = 1 << 30;
 
 static mag_status run_attend(mag_ctx* c, int32_t layer, const KvRows& rows, const void* q, int64_t ldq, void* out, int64_t ldo,
                       int32_t window, float scale) {
@@ -113,15 +113,7 @@ static mag_status run_attend(mag_ctx* c, int32_t layer, const KvRows& rows, cons
   a.part_ml = c->at_ml;
   a.arrivals = c->at_arrivals;
   const Launch L{c->stream, false, nullptr};
-  const bool tc = attend_tc_fits(a);
-  int64_t few_blocks = 0;  // pool blocks of the sessions of few rows, over the KV heads
-  for (int i = 0; i < rows.n_seg; ++i) {
-    const KvSeg& s = rows.seg[i];
-    int64_t keys = s.pos0 + s.n_tok;
-    if (window) keys = std::min<int64_t>(keys, (int64_t)window + s.n_tok);
-    if ((int64_t)s.n_tok * c->G <= kFewRows) few_blocks += (keys + 15) / 16 * c->Hkv;
-  }
-  const int few_rows = !tc ? INT32_MAX : (few_blocks <= kFewBlocks ? kFewRows : 0);
+  const int few_rows = attend_tc_fits(a) ? kFewRows : INT32_MAX;
   for (int kind = 0; kind < 3; ++kind) {
     int64_t most = 0;
     a.n_seg = 0;
