@@ -262,13 +262,14 @@ mag_status mag_verify_tokens(mag_ctx* ctx, int32_t session, int32_t n_tokens, co
  * oldest token first. They share positions, blocks and lengths with every other call on the session. The
  * rows are fp16, buffers 16-byte aligned; `ld` is the number of values from one row to the next (a multiple of 8, so a
  * part of a wider row, such as merged q, k and v, can be passed as it lies). The context's device must be
- * current. Stream-ordered; nothing is launched on error. The calls may be captured on the context's stream into a
- * CUDA graph (sessions, counts and lengths are then those of the capture; make one mag_attend of the same
- * shape before it, which allocates its workspace); replays are ordered like the calls, one after another. */
+ * current. Stream-ordered; nothing is launched on error. All but mag_session_extend may be captured on the context's
+ * stream into a CUDA graph: sessions, counts and lengths are then those of the capture, and the context's first
+ * mag_attend, which makes its workspace, has to come before it. All graphs and calls of a context share that workspace:
+ * replays are ordered like calls, one after another. */
 
 /* Make room for new tokens: session i grows by n_tokens_host[i] >= 0 tokens at its next positions, whose keys and
  * values are undefined in every layer until they are written (mag_kv_write). All sessions or none. Block-table
- * entries are copied to the device in stream order. Errors: INVALID_ARG, CONTEXT_FULL, KV_FULL, OOM, CUDA. */
+ * entries are copied to the device in stream order. Errors: INVALID_ARG (also in a capture), CONTEXT_FULL, KV_FULL, OOM, CUDA. */
 mag_status mag_session_extend(mag_ctx* ctx, int32_t n_sessions, const int32_t* session_ids_host,
                               const int32_t* n_tokens_host);
 
@@ -293,11 +294,11 @@ mag_status mag_kv_export(mag_ctx* ctx, int32_t session, int32_t first, int32_t n
  *   out[r][h] = sum_j softmax_j(scale q[r][h] . k_j) v_j,   h reading KV head h / (n_heads / n_kv_heads),
  * over the keys j <= p of a token at position p, and j > p - window when window > 0 (0: no window); k and v are the
  * fp16 values that mag_kv_read gives. q_dev is fp16 [rows][n_heads][head_dim] (already rotated), row stride ldq;
- * out_dev the same with row stride ldo; the two must not overlap. The sums, the softmax and its maximum are kept in fp32. A row's result does
- * not depend on the other sessions of the call beyond how its keys are split over blocks. Stored values must be
- * finite where any of the call's tokens, windowed or not, could lie near them (a product with 0 of an infinite
+ * out_dev the same with row stride ldo; the two must not overlap. The sums, the softmax and its maximum are kept in
+ * fp32. A row's result does not depend on the other sessions of the call beyond how its keys are split over blocks.
+ * The sessions' stored keys and values must be finite, those outside the window too (the product of 0 and an infinite
  * value is NaN); slots past a session's end may hold anything. scale must be finite.
- * Errors: INVALID_ARG, OOM (the workspace), CUDA. */
+ * Errors: INVALID_ARG (also a context's first call in a capture), OOM (the workspace), CUDA. */
 mag_status mag_attend(mag_ctx* ctx, int32_t layer, int32_t n_sessions, const int32_t* session_ids_host,
                       const int32_t* n_tokens_host, const void* q_dev, int64_t ldq, void* out_dev, int64_t ldo,
                       int32_t window, float scale);
@@ -324,7 +325,8 @@ typedef struct mag_sample_params {
  * Sums are exact in integers (w in units of 2^-40), so a result depends on nothing but its row. token_dev[row] is
  * the token's index, -1 for a row with no token to draw (none allowed, or every logit NaN or -inf; those are never
  * drawn); prob_dev[row] (may be null) its share of the kept w, NaN for a row without a token. Infinite
- * logits share all the weight. p may be null (temperature 1, no cuts).
+ * logits share all the weight. A uniform number below 0 or NaN counts as 0, one of 1 or more takes the prefix's last
+ * token. p may be null (temperature 1, no cuts). Arrays are aligned to their elements.
  * Errors: INVALID_ARG, UNSUPPORTED (vocab above 540,672 in fp16, 270,336 in fp32), CUDA. */
 mag_status mag_sample(const void* logits_dev, int32_t logits_type, int32_t rows, int32_t vocab, int64_t ld,
                       const mag_sample_params* p, const float* uniform_dev, int32_t* token_dev, float* prob_dev,

@@ -50,6 +50,14 @@ static mag_status op_device(mag_ctx* c, const char* what) {
   return MAG_OK;
 }
 
+// Work that a graph must not hold: it would be done at the capture and not again, or read host memory at a replay.
+static mag_status op_not_captured(mag_ctx* c, const char* what, const char* why) {
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  CUDA_TRY(c, cudaStreamIsCapturing(c->stream, &st));
+  if (st != cudaStreamCaptureStatusNone) return fail(c, MAG_ERR_INVALID_ARG, "%s: the stream is being captured; %s", what, why);
+  return MAG_OK;
+}
+
 // Blocks of a read: the pool blocks that each session's tokens touch.
 static int read_blocks(const KvRows& r, int32_t* blk0) {
   int n = 0;
@@ -63,6 +71,8 @@ static int read_blocks(const KvRows& r, int32_t* blk0) {
 // The workspace of split attention tiles, made by the first call that needs it.
 static mag_status attend_workspace(mag_ctx* c) {
   if (c->at_part) return MAG_OK;
+  const mag_status cap = op_not_captured(c, "attend", "make one call before the capture, which makes the workspace");
+  if (cap != MAG_OK) return cap;
   const size_t part = kAttendPartFloats * 4, ml = kAttendMlFloats * 4, cnt = kAttendArrivals * 4;
   cudaError_t e;
   float *p = nullptr, *m = nullptr;
@@ -156,6 +166,8 @@ mag_status mag_session_extend(mag_ctx* c, int32_t n, const int32_t* sids, const 
   }
   const mag_status dv = op_device(c, "session_extend");
   if (dv != MAG_OK) return dv;
+  const mag_status cap = op_not_captured(c, "session_extend", "a replay would not extend the sessions");
+  if (cap != MAG_OK) return cap;
   const mag_status st = reserve_blocks(c, "session_extend", need);
   if (st != MAG_OK) return st;
   for (int i = 0; i < n; ++i) {
@@ -261,6 +273,10 @@ mag_status mag_sample(const void* logits, int32_t type, int32_t rows, int32_t vo
   if (rows == 0) return MAG_OK;
   const uintptr_t at = reinterpret_cast<uintptr_t>(logits);
   if (!logits || !uniform || !token || at % (f32 ? 4 : 2)) return MAG_ERR_INVALID_ARG;
+  const void* words[] = {uniform, token, prob, p ? p->temperature : nullptr, p ? (const void*)p->top_k : nullptr,
+                         p ? p->top_p : nullptr, p ? p->min_p : nullptr, p ? (const void*)p->allowed : nullptr};
+  for (const void* w : words)
+    if (reinterpret_cast<uintptr_t>(w) % 4) return MAG_ERR_INVALID_ARG;
   SampleArgs a = {};
   a.logits = logits;
   a.ld = ld;

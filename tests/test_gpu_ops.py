@@ -374,6 +374,113 @@ def test_attend_captured_graph_replays():
             assert torch.equal(out, eager)
 
 
+@pytest.mark.parametrize("kv", ALL_KV, ids=KV_NAMES.get)
+@pytest.mark.parametrize("group,new", [(1, 15), (1, 16), (1, 17), (1, 127), (1, 128), (1, 129), (1, 256), (1, 257), (3, 5),
+                                       (3, 6), (3, 42), (3, 43), (3, 85), (3, 86), (8, 2), (8, 3), (8, 16), (8, 17),
+                                       (8, 32), (8, 33)])
+def test_attend_at_every_tile_border(kv, group, new):
+    """Packed rows on both sides of 16, 128 and 256, over keys that are cut into several blocks' parts, with and without a
+    window."""
+    for dim, window in ((64, 0), (128, 700)):
+        attend_case(kv, group, 1, dim, [2100], [new], window=window, seed=new)
+
+
+def test_attend_two_graphs_and_calls_share_the_workspace():
+    """Two captured graphs of one context, replayed in turn with a call between them, give the bits of eager calls."""
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        ctx, sids, q, out = attend_case(mag.KV_INT8, 4, 1, 128, [3000, 2500, 2000], [3, 30, 200], seed=8, ctx=make(
+            mag.KV_INT8, 4, 1, 128, pool_blocks=520, max_context=3100, stream=stream.cuda_stream))
+        eager = [torch.empty_like(out) for _ in range(2)]
+        calls = ((sids[:2], [3, 30], q), (sids[1:], [30, 200], q[3:]))
+        for c, e in zip(calls, eager):
+            ctx.attend(0, *c, e)
+        ctx.sync()
+        graphs, outs = [], []
+        for c in calls:
+            o, g = torch.empty_like(out), torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=stream):
+                ctx.attend(0, *c, o)
+            graphs.append(g)
+            outs.append(o)
+        for _ in range(3):
+            for i, (g, o, n) in enumerate(zip(graphs, outs, (33, 230))):
+                o.zero_()
+                g.replay()
+                ctx.attend(0, sids, [3, 30, 200], q, out)
+                ctx.sync()
+                assert torch.equal(o[:n], eager[i][:n])
+
+
+def test_what_a_capture_refuses():
+    """A context's first attend (it makes the workspace) and every session_extend; the capture goes on."""
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        ctx = make(mag.KV_FP16, 4, 2, 64, stream=stream.cuda_stream)
+        sid = ctx.session_open()
+        ctx.session_extend([sid], [20])
+        k, q = torch.zeros((20, 2, 64), device="cuda").half(), torch.zeros((20, 4, 64), device="cuda").half()
+        out = torch.ones_like(q)
+        ctx.kv_write(0, [sid], [20], k, k)
+        ctx.sync()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            for call in (lambda: ctx.attend(0, [sid], [20], q, out), lambda: ctx.session_extend([sid], [1])):
+                with pytest.raises(mag.MagError) as e:
+                    call()
+                assert e.value.status == mag.ERR_INVALID_ARG
+            ctx.kv_write(0, [sid], [20], k, k)
+        graph.replay()
+        ctx.sync()
+        assert ctx.session_length(sid) == 20
+        ctx.attend(0, [sid], [20], q, out)
+        ctx.sync()
+        assert (out == 0).all()
+
+
+def test_attend_without_memory_for_the_workspace():
+    ctx = make(mag.KV_FP16, 4, 2, 64)
+    sid = ctx.session_open()
+    ctx.session_extend([sid], [20])
+    k, q = torch.ones((20, 2, 64), device="cuda").half(), torch.zeros((20, 4, 64), device="cuda").half()
+    ctx.kv_write(0, [sid], [20], k, k)
+    out = torch.zeros_like(q)
+    before = ctx.memory_stats()["other_device_bytes"]
+    for skip in range(3):
+        mag.debug_fail_allocations(skip, 1)
+        try:
+            with pytest.raises(mag.MagError) as e:
+                ctx.attend(0, [sid], [20], q, out)
+        finally:
+            mag.debug_fail_allocations(0, 0)
+        assert e.value.status == mag.ERR_OOM and ctx.memory_stats()["other_device_bytes"] == before
+    ctx.attend(0, [sid], [20], q, out)
+    ctx.sync()
+    assert (out == 1).all() and ctx.memory_stats()["other_device_bytes"] > before
+
+
+@pytest.mark.parametrize("kv", ALL_KV, ids=KV_NAMES.get)
+def test_elastic_pool_grows_under_extension(kv):
+    """Sessions of an elastic pool, which maps its blocks as they are asked for: extended, written, attended and read."""
+    rng = np.random.default_rng(3)
+    ctx = make(kv, 4, 2, 64, pool_blocks=2048, max_context=20000, flags=mag.FLAG_ELASTIC_POOL)
+    mapped = ctx.memory_stats()["pool_blocks_mapped"]
+    n = min(19000, (mapped + 1) * 16 + 5)
+    sid = ctx.session_open()
+    k, v = half(rng, n, 2, 64), half(rng, n, 2, 64)
+    ctx.session_extend([sid], [n])
+    ctx.kv_write(0, [sid], [n], k.cuda(), v.cuda())
+    kr, vr = torch.empty((2, n, 2, 64), dtype=torch.float16, device="cuda")
+    ctx.kv_read(0, [sid], [n], kr, vr)
+    q = half(rng, 3, 4, 64)
+    out = torch.empty((3, 4, 64), dtype=torch.float16, device="cuda")
+    ctx.attend(0, [sid], [3], q.cuda(), out)
+    ctx.sync()
+    ks, vs = as_stored(k, kv), as_stored(v, kv)
+    assert torch.equal(kr.cpu(), ks) and torch.equal(vr.cpu(), vs)
+    check(out, *reference(q, ks, vs, n - 3, 0, 0.125), 2)
+
+
 # ------------------------------------------------------------------------------------------------ sampling
 def sample_reference(logits, t, k, p, m, u, allowed):
     """One row in 64 bits; returns (token, probability)."""
@@ -483,6 +590,39 @@ def test_sample_ties(dtype):
     sample_case(x, t=0.5, k=2950, u=u)
     sample_case(x, t=0.5, p=0.9999, u=u)
     sample_case(x, m=1.0, u=u)
+
+
+@pytest.mark.parametrize("dtype", [np.float16, np.float32])
+def test_sample_numbers_outside_the_unit_interval(dtype):
+    """No uniform number takes the draw out of what the cuts keep."""
+    x = rows_of(np.random.default_rng(6), 6, 4000, dtype)
+    u = torch.tensor([math.nan, -1.0, 1.0, 2.0, math.inf, -math.inf], device="cuda")
+    token = torch.full((6,), -7, dtype=torch.int32, device="cuda")
+    mag.sample(torch.from_numpy(x).cuda(), 6, 4000, u, token, stream=torch.cuda.current_stream().cuda_stream,
+               dtype=mag.LOGITS_F32 if dtype == np.float32 else mag.LOGITS_F16,
+               top_k=torch.full((6,), 5, dtype=torch.int32, device="cuda"))
+    for row, t in zip(x, token.cpu().tolist()):
+        assert t in np.argsort(-row.astype(np.float64), kind="stable")[:5]
+
+
+def test_sample_captured_on_another_stream():
+    rng = np.random.default_rng(12)
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        x, u = torch.from_numpy(rows_of(rng, 5, 3000, np.float16)).cuda(), torch.rand(5, device="cuda")
+        token, eager = torch.empty((2, 5), dtype=torch.int32, device="cuda")
+        p = torch.full((5,), 0.9, device="cuda")
+        mag.sample(x, 5, 3000, u, eager, top_p=p, stream=stream.cuda_stream)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            mag.sample(x, 5, 3000, u, token, top_p=p, stream=stream.cuda_stream)
+        for _ in range(3):
+            x.copy_(torch.from_numpy(rows_of(rng, 5, 3000, np.float16)))
+            u.copy_(torch.rand(5))
+            graph.replay()
+            mag.sample(x, 5, 3000, u, eager, top_p=p, stream=stream.cuda_stream)
+            stream.synchronize()
+            assert torch.equal(token, eager)
 
 
 @pytest.mark.parametrize("dtype", [np.float16, np.float32])

@@ -44,3 +44,16 @@ def test_lists_of_unlike_length():
         mag._Lists([1, 2], [3])
     a = mag._Lists([5, 6], [7, 8])
     assert a.n == 2 and list((ctypes.c_int32 * 4).from_address(a.ids)) == [5, 6, 7, 8] and a.counts == a.ids + 8
+
+
+def test_sample_refuses_misaligned_arrays(lib):
+    x = 4096
+    for name in ("uniform", "token", "prob", "temperature", "top_k", "top_p", "min_p", "allowed"):
+        at = dict(uniform=x, token=x, prob=x)
+        p = mag.SampleParams()
+        if name in at:
+            at[name] = x + 2
+        else:
+            setattr(p, name, x + 2)
+        assert lib.mag_sample(x, mag.LOGITS_F16, 1, 16, 16, ctypes.byref(p), at["uniform"], at["token"], at["prob"],
+                              None) == mag.ERR_INVALID_ARG, name
