@@ -50,10 +50,6 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
 __device__ __forceinline__ __half2 s8_pair(uint32_t w, uint32_t sel) {
   return __hsub2(u32_as_h2(prmt(w, 0x64646464u, sel)), u32_as_h2(0x64806480u));
 }
-__device__ __forceinline__ __half2 u4_pair(uint32_t w, int i) {  // nibbles i and i + 4 of a word
-  return __hsub2(u32_as_h2(((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u), u32_as_h2(0x64006400u));
-}
-
 // One pool block (16 tokens of one head) as lane (g, t) holds it.
 template <int D, int KV>
 struct Raw {
@@ -188,8 +184,7 @@ __device__ __forceinline__ uint32_t v_pair(const uint32_t (&a)[Raw<D, KV>::VW], 
     return h2_as_u32(__hmul2(s8_pair(x, (n & 1) ? 0x4342 : 0x4140), s));
   } else {
     const uint32_t x = prmt(a[n >> 3], b[n >> 3], (n & 4) ? 0x7632 : 0x5410);
-    const __half2 q = __hsub2(u32_as_h2(((x >> (4 * (n & 3))) & 0x000F000Fu) | 0x64006400u), u32_as_h2(0x64006400u));
-    return h2_as_u32(__hfma2(q, s, m));
+    return h2_as_u32(__hfma2(u4_pair(x, n & 3), s, m));
   }
 }
 

@@ -192,8 +192,7 @@ struct Ring : RingShape<D, KV> {
             uint32_t v[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              v[k] = h2_as_u32(__hfma2(
-                  __hsub2(u32_as_h2(((cw[e] >> (4 * k)) & 0x000F000Fu) | 0x64006400u), u32_as_h2(0x64006400u)), sc, mn));
+              v[k] = h2_as_u32(__hfma2(u4_pair(cw[e], k), sc, mn));
             const int cc = 4 * run + e;
             *reinterpret_cast<uint4*>(row_p + (cc >> 3) * S::kHalf + (((cc & 7) ^ (row & 7)) << 4)) =
                 make_uint4(v[0], v[1], v[2], v[3]);

@@ -105,9 +105,7 @@ __device__ __forceinline__ uint4 expand8(const uint8_t* data, uint32_t meta) {
     const uint32_t c = *reinterpret_cast<const uint32_t*>(data);
     const __half2 s = __low2half2(u32_as_h2(meta)), m = __high2half2(u32_as_h2(meta));
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      r[i] = h2_as_u32(
-          __hfma2(__hsub2(u32_as_h2(((c >> (4 * i)) & 0x000F000Fu) | 0x64006400u), u32_as_h2(0x64006400u)), s, m));
+    for (int i = 0; i < 4; ++i) r[i] = h2_as_u32(__hfma2(u4_pair(c, i), s, m));
     return make_uint4(__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[2], r[3], 0x5410),
                       __byte_perm(r[0], r[1], 0x7632), __byte_perm(r[2], r[3], 0x7632));
   }

@@ -206,10 +206,7 @@ __global__ void __launch_bounds__(kIoThreads) kv_read_kernel(const KvReadArgs a)
       const __half2 sc = __low2half2(sm), mn = __high2half2(sm);
       uint32_t r[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // codes (i, i + 4) as fp16 1024 + q
-        const uint32_t h = ((c >> (4 * i)) & 0x000F000Fu) | 0x64006400u;
-        r[i] = h2_as_u32(__hfma2(__hsub2(u32_as_h2(h), u32_as_h2(0x64006400u)), sc, mn));
-      }
+      for (int i = 0; i < 4; ++i) r[i] = h2_as_u32(__hfma2(u4_pair(c, i), sc, mn));
       o = make_uint4(__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[2], r[3], 0x5410),
                      __byte_perm(r[0], r[1], 0x7632), __byte_perm(r[2], r[3], 0x7632));
     }

@@ -8,6 +8,16 @@
 
 namespace mag {
 
+#ifdef __CUDACC__
+// Codes of nibbles i and i + 4 of a word of INT4 codes as an fp16 pair, exact: 1024 + q less 1024, or, of odd nibbles,
+// (1024 + 16 q) / 16 less 64, which saves their shift.
+__device__ __forceinline__ __half2 u4_pair(uint32_t w, int i) {
+  const uint32_t x = i < 2 ? w : w >> 8;
+  return i & 1 ? __hfma2(u32_as_h2((x & 0x00F000F0u) | 0x64006400u), u32_as_h2(0x2C002C00u), u32_as_h2(0xD400D400u))
+               : __hsub2(u32_as_h2((x & 0x000F000Fu) | 0x64006400u), u32_as_h2(0x64006400u));
+}
+#endif
+
 // Launch helper: every kernel goes through cudaLaunchKernelEx so that the
 // programmatic-dependent-launch attribute can be set uniformly.
 struct Launch {
