@@ -87,25 +87,22 @@ __device__ __forceinline__ void for_share(const AttendArgs& a, const AttendShare
   }
 }
 
-// 8 stored values as fp16 in order.
+// 8 stored values (INT8: words c0 and c1, offset by 128; INT4: word c0) as fp16 in order.
 template <int KV>
-__device__ __forceinline__ uint4 expand8(const uint8_t* data, uint32_t meta) {
+__device__ __forceinline__ uint4 expand8(uint32_t c0, uint32_t c1, uint32_t meta) {
   uint32_t r[4];
+  const __half2 s = __low2half2(u32_as_h2(meta));
   if constexpr (KV == 1) {
-    const uint2 c = *reinterpret_cast<const uint2*>(data);
-    const uint32_t cw[2] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u};
-    const __half2 s = __low2half2(u32_as_h2(meta));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t h = __byte_perm(cw[i >> 1], 0x64646464u, (i & 1) ? 0x4342 : 0x4140);
+      const uint32_t h = __byte_perm((i < 2 ? c0 : c1) ^ 0x80808080u, 0x64646464u, (i & 1) ? 0x4342 : 0x4140);
       r[i] = h2_as_u32(__hmul2(__hsub2(u32_as_h2(h), u32_as_h2(0x64806480u)), s));
     }
     return make_uint4(r[0], r[1], r[2], r[3]);
   } else {
-    const uint32_t c = *reinterpret_cast<const uint32_t*>(data);
-    const __half2 s = __low2half2(u32_as_h2(meta)), m = __high2half2(u32_as_h2(meta));
+    const __half2 m = __high2half2(u32_as_h2(meta));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = h2_as_u32(__hfma2(u4_pair(c, i), s, m));
+    for (int i = 0; i < 4; ++i) r[i] = h2_as_u32(__hfma2(u4_pair(c0, i), s, m));
     return make_uint4(__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[2], r[3], 0x5410),
                       __byte_perm(r[0], r[1], 0x7632), __byte_perm(r[2], r[3], 0x7632));
   }
@@ -312,10 +309,15 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
       mb_wait(mma_done, 0);
     }
   } else if (KV != 0 && warp >= 12) {
-    // ---- expansion of INT8 / INT4 tiles, 8 values a thread at a time
+    // ---- expansion of INT8 / INT4 tiles, 16 stored bytes of a row a thread at a time
     regs_dec<C::kRegsOther>();
     if constexpr (KV != 0) {
       const int w = warp - 12;
+      // 8 lanes side by side have 8 rows, and of each the run that makes the banks that they read differ; the runs that
+      // they write differ then too (64 INT4 values: two by two the same)
+      constexpr int kRuns = C::kRowB / 16;
+      const int b1 = (lane >> 1) & 1, b2 = (lane >> 2) & 1;
+      const int turn = C::kRowB == 128 ? lane & 7 : (C::kRowB == 32 ? b2 : (KV == 1 ? 2 * b1 + (b2 ^ b1) : 2 * b2 + b1));
       int g = 0;
       for_share(a, sh, [&](const Unit& x, int, int s0, int s1) {
         const int len = x.sg.pos0 + x.sg.n_tok;
@@ -329,19 +331,25 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
             }
             const uint8_t* src = raw + r * C::kRawBytes;
             uint8_t* dst = ring + st * C::kTile;
-#pragma unroll 4
-            for (int i = 0; i < kKeys * D / 8 / 128; ++i) {
-              // 8 lanes a 128-byte row of a half, 4 rows a warp
-              const int item = i * 16 + w * 4 + (lane >> 3);
-              const int row = item % kKeys, c = (item / kKeys) * 8 + (lane & 7);
-              uint4 v = make_uint4(0, 0, 0, 0);
+#pragma unroll 2
+            for (int i = 0; i < kKeys * kRuns / 128; ++i) {
+              const int item = (i * 4 + w) * 32 + lane, row = (item & 7) | (item / (8 * kRuns) << 3);
+              const int run = ((item >> 3) % kRuns) ^ turn;
+              uint4 c = make_uint4(0, 0, 0, 0);
+              uint32_t meta = 0;
               if (row < live) {
+                c = *reinterpret_cast<const uint4*>(src + row * C::kRowB + 16 * run);
                 const uint8_t* mp = src + C::kRawData + row * C::kMetaB;
-                const uint32_t meta = KV == 1 ? *reinterpret_cast<const uint16_t*>(mp)
-                                              : reinterpret_cast<const uint32_t*>(mp)[c >> 2];
-                v = expand8<KV>(src + row * C::kRowB + c * (KV == 1 ? 8 : 4), meta);
+                meta = KV == 1 ? *reinterpret_cast<const uint16_t*>(mp) : reinterpret_cast<const uint32_t*>(mp)[run];
               }
-              *reinterpret_cast<uint4*>(dst + (c >> 3) * C::kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
+              const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+              constexpr int NE = KV == 1 ? 2 : 4;  // fp16 runs of a stored one
+#pragma unroll
+              for (int e = 0; e < NE; ++e) {
+                const int cc = NE * run + e;
+                const uint4 v = KV == 1 ? expand8<KV>(cw[2 * (e & 1)], cw[2 * (e & 1) + 1], meta) : expand8<KV>(cw[e], 0, meta);
+                *reinterpret_cast<uint4*>(dst + (cc >> 3) * C::kHalf + row * 128 + (((cc & 7) ^ (row & 7)) << 4)) = v;
+              }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
