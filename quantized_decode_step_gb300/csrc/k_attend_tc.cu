@@ -45,8 +45,10 @@ struct Cfg {
   static constexpr int kRaw = KV == 0 ? 0 : 2;         // slots of raw bytes
   static constexpr int kRawBytes = KV == 0 ? 0 : kRawData + kRawMeta;
   static constexpr int kThreads = KV == 0 ? 384 : 512;
-  // registers: 384 x 168 or 512 x 128 at launch
-  static constexpr int kRegsSoftmax = KV == 0 ? 200 : 184, kRegsOther = KV == 0 ? 104 : 72;
+  // registers: 384 x 168 or 512 x 128 at launch. The softmax wants them (256 tokens on 20,000 INT4 keys: 96 us so, 100 at
+  // 184 and 72, 133 at 168 and 88); FP16 is the same from 200 to 216.
+  static constexpr int kRegsSoftmax = 200, kRegsOther = KV == 0 ? 104 : 56;
+  static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * (KV == 0 ? 168 : 128), "registers");
   static constexpr int kBars = 2 * kStages + 2 * kRaw + 9;
   static constexpr int kSmem = 2 * kTile + kStages * kTile + kRaw * kRawBytes + kBars * 8 + 64 + 1024;
 };
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
             }
             const uint8_t* src = raw + r * C::kRawBytes;
             uint8_t* dst = ring + st * C::kTile;
-#pragma unroll 2
+#pragma unroll 1
             for (int i = 0; i < kKeys * kRuns / 128; ++i) {
               const int item = (i * 4 + w) * 32 + lane, row = (item & 7) | (item / (8 * kRuns) << 3);
               const int run = ((item >> 3) % kRuns) ^ turn;
