@@ -275,7 +275,8 @@ mag_status mag_session_extend(mag_ctx* ctx, int32_t n_sessions, const int32_t* s
 
 /* Store already-rotated keys and values [rows][n_kv_heads][head_dim] of one layer for the sessions' newest tokens,
  * quantised as they are written to the same bytes as by mag_kv_append. Tokens may be written again. The values of an
- * INT8 or INT4 pool must be finite. k_dev and v_dev have the same row stride. Errors: INVALID_ARG, CUDA. */
+ * INT8 or INT4 pool must be finite; those above 65,440 in magnitude may read back as infinite (the scale is rounded).
+ * k_dev and v_dev have the same row stride. Errors: INVALID_ARG, CUDA. */
 mag_status mag_kv_write(mag_ctx* ctx, int32_t layer, int32_t n_sessions, const int32_t* session_ids_host,
                         const int32_t* n_tokens_host, const void* k_dev, const void* v_dev, int64_t ld);
 

@@ -181,7 +181,7 @@ struct mag_ctx {
   float* pf_part = nullptr;     // split-K GEMMs: partial sums of the two K halves
   uint32_t* pf_part_cnt = nullptr;
   float* pf_last_r = nullptr;   // [MAG_MAX_BATCH][D]: the sessions' last residual rows, gathered
-  // mag_attend's workspace (split tiles), allocated by the first call that splits
+  // mag_attend's workspace (parts of cut tiles), made by the context's first call
   float* at_part = nullptr;
   float* at_ml = nullptr;
   uint32_t* at_arrivals = nullptr;
