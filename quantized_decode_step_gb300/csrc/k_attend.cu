@@ -493,9 +493,7 @@ cudaError_t launch_few_t(const Launch& L, const AttendArgs& a, const AttendShare
   constexpr int W = few_warps<D, KV, NT>(), smem = sizeof(FewSmem<D, NT, W>);
   cudaError_t e = cudaFuncSetAttribute(attend_few_kernel<D, KV, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  attend_few_kernel<D, KV, NT><<<sh.n, W * 32, smem, L.stream>>>(a, sh);
-  if (L.counter) ++*L.counter;
-  return cudaGetLastError();
+  return launch_kernel(L, attend_few_kernel<D, KV, NT>, dim3(sh.n), dim3(W * 32), smem, a, sh);
 }
 template <int D, int KV>
 cudaError_t launch_few_nt(const Launch& L, const AttendArgs& a, const AttendShares& sh, int tile_rows) {

@@ -84,17 +84,8 @@ __global__ void __launch_bounds__(kWarps * 32) attend_merge_kernel(const __grid_
 
 template <int D, bool PERM>
 cudaError_t launch_merge_t(const Launch& L, const AttendArgs& a, const AttendCuts& cuts, int tiles) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cuts.n * tiles * 4 * (D / 64));
-  cfg.blockDim = dim3(kWarps * 32);
-  cfg.stream = L.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (L.counter) ++*L.counter;
-  return cudaLaunchKernelEx(&cfg, attend_merge_kernel<D, PERM>, a, cuts, tiles);
+  return launch_kernel(Launch{L.stream, true, L.counter}, attend_merge_kernel<D, PERM>, dim3(cuts.n * tiles * 4 * (D / 64)),
+                       dim3(kWarps * 32), 0, a, cuts, tiles);
 }
 
 }  // namespace

@@ -598,9 +598,7 @@ cudaError_t launch_stream_t(const Launch& L, const AttendArgs& a, const AttendSh
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(attend_stream_kernel<D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  attend_stream_kernel<D, KV><<<sh.n, C::kThreads, C::kSmem, L.stream>>>(map, a, sh);
-  if (L.counter) ++*L.counter;
-  e = cudaGetLastError();
+  e = launch_kernel(L, attend_stream_kernel<D, KV>, dim3(sh.n), dim3(C::kThreads), C::kSmem, map, a, sh);
   return e == cudaSuccess ? launch_attend_merge(L, a, sh, 1, KV == 2) : e;
 }
 template <int D>

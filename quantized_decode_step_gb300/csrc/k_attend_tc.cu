@@ -541,9 +541,7 @@ cudaError_t launch_tc_t(const Launch& L, const AttendArgs& a, const AttendShares
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(attend_tc_kernel<D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  attend_tc_kernel<D, KV><<<sh.n, C::kThreads, C::kSmem, L.stream>>>(map, a, sh);
-  if (L.counter) ++*L.counter;
-  e = cudaGetLastError();
+  e = launch_kernel(L, attend_tc_kernel<D, KV>, dim3(sh.n), dim3(C::kThreads), C::kSmem, map, a, sh);
   return e == cudaSuccess ? launch_attend_merge(L, a, sh, 2, false) : e;
 }
 template <int D>

@@ -222,10 +222,8 @@ static cudaError_t launch_write_t(const Launch& L, const KvWriteArgs& a) {
   // one row a block leaves no load waiting for another row's; of many rows, four a block keep more bytes in flight
   // (7,000 rows of 8 heads, d 128, INT4, with their read-back: 28.3 us for 32.4; 16 rows of INT8: 9.6 us for 7.7)
   const int n = a.rows.n_rows;
-  if (n <= 512) kv_write_kernel<KV, 1><<<n, kIoThreads, 0, L.stream>>>(a);
-  else kv_write_kernel<KV, 4><<<(n + 3) / 4, kIoThreads, 0, L.stream>>>(a);
-  if (L.counter) ++*L.counter;
-  return cudaGetLastError();
+  return n <= 512 ? launch_kernel(L, kv_write_kernel<KV, 1>, dim3(n), dim3(kIoThreads), 0, a)
+                  : launch_kernel(L, kv_write_kernel<KV, 4>, dim3((n + 3) / 4), dim3(kIoThreads), 0, a);
 }
 
 cudaError_t launch_kv_write(const Launch& L, const KvWriteArgs& a) {
@@ -238,11 +236,8 @@ cudaError_t launch_kv_read(const Launch& L, const KvReadArgs& a, int n_layers) {
   if (a.n_blocks < 1 || n_layers < 1 || n_layers > 65535 || a.rows.n_seg < 1 || a.rows.n_seg > MAG_MAX_BATCH)
     return cudaErrorInvalidValue;
   const dim3 grid(a.n_blocks, 2, n_layers);
-  if (a.pool.kv_dtype == 0) kv_read_kernel<0><<<grid, kIoThreads, 0, L.stream>>>(a);
-  else if (a.pool.kv_dtype == 1) kv_read_kernel<1><<<grid, kIoThreads, 0, L.stream>>>(a);
-  else kv_read_kernel<2><<<grid, kIoThreads, 0, L.stream>>>(a);
-  if (L.counter) ++*L.counter;
-  return cudaGetLastError();
+  return launch_kernel(L, a.pool.kv_dtype == 0 ? kv_read_kernel<0> : (a.pool.kv_dtype == 1 ? kv_read_kernel<1> : kv_read_kernel<2>),
+                       grid, dim3(kIoThreads), 0, a);
 }
 
 }  // namespace mag

@@ -178,18 +178,7 @@ __global__ void f16_tiles_kernel(const __half* __restrict__ src, int N, int K, u
 
 template <typename K, typename... Args>
 cudaError_t launch_plain(const Launch& L, K kern, dim3 grid, dim3 block, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = 0;
-  cfg.stream = L.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = L.pdl ? 1 : 0;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (L.counter) ++*L.counter;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
+  return launch_kernel(L, kern, grid, block, 0, args...);
 }
 
 }  // namespace
@@ -200,9 +189,8 @@ cudaError_t launch_quantize_w4g32(cudaStream_t s, const float* src, int64_t rows
   const int64_t n = rows * groups;
   if (n == 0) return cudaSuccess;
   const int threads = 128;
-  quantize_w4g32_kernel<<<(unsigned)((n + threads - 1) / threads), threads, 0, s>>>(src, rows, cols, groups, codes,
-                                                                                      sm);
-  return cudaGetLastError();
+  return launch_plain(Launch{s, false, nullptr}, quantize_w4g32_kernel, dim3((unsigned)((n + threads - 1) / threads)),
+                      dim3(threads), src, rows, cols, groups, codes, sm);
 }
 
 cudaError_t launch_step_begin(const Launch& L, const StepArgs* step, float* r, int D, int32_t* tables,
@@ -223,8 +211,8 @@ static cudaError_t launch_tiles(cudaStream_t s, const uint8_t* src, uint8_t* dst
                                 int dir) {
   const int64_t n = (int64_t)(N / 16) * ((K + 63) / 64) * 32;
   if (n == 0) return cudaSuccess;
-  w4_tiles_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(src, dst, N, K, map, map_arg, dir);
-  return cudaGetLastError();
+  return launch_plain(Launch{s, false, nullptr}, w4_tiles_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), src, dst, N,
+                      K, map, map_arg, dir);
 }
 
 cudaError_t launch_w4_to_tiles(cudaStream_t s, const uint8_t* canon, int N, int K, int map, int map_arg,
@@ -244,7 +232,7 @@ namespace mag {
 cudaError_t launch_f16_to_tiles(cudaStream_t s, const __half* src, int N, int K, uint8_t* tiles) {
   const int64_t n = (int64_t)(N / 16) * ((K + 63) / 64) * 64;
   if (n == 0) return cudaSuccess;
-  f16_tiles_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(src, N, K, tiles);
-  return cudaGetLastError();
+  return launch_plain(Launch{s, false, nullptr}, f16_tiles_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), src, N, K,
+                      tiles);
 }
 }  // namespace mag

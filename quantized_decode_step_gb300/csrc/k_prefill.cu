@@ -715,9 +715,7 @@ cudaError_t launch_tc_gemm(const Launch& L, const void* map_a, const TcGemmArgs&
 
 cudaError_t launch_rows_to_resid(const Launch& L, const __half* x, float* r, int T, int D) {
   if (T == 0) return cudaSuccess;
-  rows_to_resid_kernel<<<T, 256, 0, L.stream>>>(x, r, D);
-  if (L.counter) ++*L.counter;
-  return cudaGetLastError();
+  return launch_kernel(Launch{L.stream, false, L.counter}, rows_to_resid_kernel, dim3(T), dim3(256), 0, x, r, D);
 }
 
 cudaError_t launch_gather_rows(const Launch& L, const float* src, int D, const RowList& rows, float* dst) {

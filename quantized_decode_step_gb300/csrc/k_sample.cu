@@ -1365,8 +1365,7 @@ cudaError_t launch_sample_t(cudaStream_t s, const SampleArgs& a) {
       constexpr int smem = (int)std::max(sizeof(CountSmem), sizeof(SampleSmem<1>));
       e = cudaFuncSetAttribute(sample_counted_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return e;
-      sample_counted_kernel<<<a.rows, kCountThreads, smem, s>>>(a);
-      return cudaGetLastError();
+      return launch_kernel(Launch{s, false, nullptr}, sample_counted_kernel, dim3(a.rows), dim3(kCountThreads), smem, a);
     }
   }
   // a row or more for every SM: a block a row

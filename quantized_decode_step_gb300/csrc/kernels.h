@@ -25,6 +25,25 @@ struct Launch {
   bool pdl;
   int* counter;  // incremented per launch (may be null)
 };
+#ifdef __CUDACC__
+// A launch and its own status: cudaGetLastError() would also give what an earlier failed call of this thread left (an
+// allocation that was refused and handled, say).
+template <typename K, typename... Args>
+cudaError_t launch_kernel(const Launch& L, K kern, dim3 grid, dim3 block, size_t smem, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = L.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = L.pdl ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (L.counter) ++*L.counter;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+#endif
 
 // ---------------------------------------------------------------- W4 / fp16 GEMV (mma.sync)
 enum WeightFmt { W_W4 = 0, W_F16 = 1 };
