@@ -547,7 +547,8 @@ mag_status mag_debug_timeline(mag_ctx* ctx, int32_t batch, const int32_t* sessio
                               void* out_dev, void* recs_dev, int32_t cap, int32_t* n_out);
 
 /* Failure injection for tests ([Magnitude] 5.1-5.2: the engine's error behaviour): the number of polls a
- * decode GEMV's pipeline wait (for its weight copies to land in shared memory) makes before it gives up.
+ * decode GEMV's pipeline wait (for its weight copies to land in shared memory) makes before it gives up, and of
+ * the waits between the roles of the prefill GEMM and of mag_attend's kernels for more than 16 packed rows.
  * polls < 0 restores the built-in limit (2^22); 0 makes every such wait give up at once, as if the copies
  * were stuck: the kernel then sets its bit in the error word, waits (within the built-in limit) for the
  * copies it has in flight, skips its arithmetic and returns, so the step's outputs are meaningless, the

@@ -21,8 +21,9 @@ __device__ __forceinline__ void mb_expect(uint64_t* b, uint32_t bytes) {
 __device__ __forceinline__ void mb_arrive(uint64_t* b) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(b)) : "memory");
 }
-__device__ __forceinline__ bool mb_wait(uint64_t* b, uint32_t par) {
-  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+// Bounded wait for the phase of parity `par`: at most `limit` polls of up to a microsecond.
+__device__ __forceinline__ bool mb_wait(uint64_t* b, uint32_t par, uint32_t limit = kWaitPolls) {
+  for (uint32_t i = 0; i < limit; ++i) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\tselp.u32 %0, 1, 0, p;\n\t}"
@@ -32,6 +33,11 @@ __device__ __forceinline__ bool mb_wait(uint64_t* b, uint32_t par) {
     if (ok) return true;
   }
   return false;
+}
+// The same by all lanes of a warp, which go on or give up together: each polls for itself, and where the phase completes
+// around the last poll only some see it.
+__device__ __forceinline__ bool mb_wait_warp(uint64_t* b, uint32_t par, uint32_t limit) {
+  return __all_sync(0xffffffffu, mb_wait(b, par, limit));
 }
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile(
@@ -149,10 +155,10 @@ __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 // A barrier of the warps that `bar` counts, bounded like every wait: false where one of them did not come.
-__device__ __forceinline__ bool join(uint64_t* bar, int& phase) {
+__device__ __forceinline__ bool join(uint64_t* bar, int& phase, uint32_t limit) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mb_arrive(bar);
-  return mb_wait(bar, phase++ & 1);
+  return mb_wait_warp(bar, phase++ & 1, limit);
 }
 
 // The tensor map of one layer's FP16 pool: rows of D values, [block][K, V][head][16], boxes of 16 rows and 64 values.

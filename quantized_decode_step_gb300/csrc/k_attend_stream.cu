@@ -103,7 +103,7 @@ struct Ring : RingShape<D, KV> {
         const int id_w = ids[part], id_at = (s - at[part]) * 8;
         const int my = __shfl_sync(0xffffffffu, id_w, id_at + (lane & 7));
         const int st = g % S::kStages;
-        if (g >= S::kStages && !mb_wait(empty + st, ((g / S::kStages) - 1) & 1)) {
+        if (g >= S::kStages && !mb_wait_warp(empty + st, ((g / S::kStages) - 1) & 1, a.wait_limit)) {
           if (lane == 0) atomicOr(a.err, kErrAttend);
           return false;
         }
@@ -159,7 +159,7 @@ struct Ring : RingShape<D, KV> {
     int ge = 0;  // and expanded
     auto expand_next = [&] {
       const int st = ge % S::kStages, r = ge % S::kRaw;
-      if (ge >= S::kStages && !mb_wait(empty + st, ((ge / S::kStages) - 1) & 1)) {
+      if (ge >= S::kStages && !mb_wait_warp(empty + st, ((ge / S::kStages) - 1) & 1, a.wait_limit)) {
         if (lane == 0) atomicOr(a.err, kErrAttend);
         return false;
       }
@@ -365,11 +365,11 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
       int g = 0, piece = 0, cnt[2] = {0, 0};
       const uint32_t q_a = su32(q_s), ring_a = su32(ring.tiles);
       for_share(a, sh, [&](const Unit&, int, int s0, int s1) {
-        bool ok = mb_wait(q_full, piece & 1);
+        bool ok = mb_wait(q_full, piece & 1, a.wait_limit);
         ++piece;
         ok = ok && in_order(s0, s1, [&](int s, int part) {
           const int t = (s - s0) & 1, st = g % C::kStages;
-          if (!mb_wait(ring.full + st, (g / C::kStages) & 1)) return false;
+          if (!mb_wait(ring.full + st, (g / C::kStages) & 1, a.wait_limit)) return false;
           if (part == 0) {
             tc_after();
             const uint64_t qd = smem_desc(q_a, 16), kd = smem_desc(ring_a + st * C::kTile, 16);
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
             }
             mma_commit(s_full + t);
           } else {
-            if (!mb_wait(p_full + t, cnt[t] & 1)) return false;
+            if (!mb_wait(p_full + t, cnt[t] & 1, a.wait_limit)) return false;
             ++cnt[t];
             tc_after();
             const uint64_t vd = smem_desc(ring_a + st * C::kTile, C::kHalf);
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
     auto token_of = [&](int r) { return G == 1 ? r : (int)__umulhi((uint32_t)r, g_inv); };
     int cnt = 0, n_o = 0, n_join = 0;
     auto all = [&] {
-      const bool ok = join(joined, n_join);
+      const bool ok = join(joined, n_join, a.wait_limit);
       if (!ok && lane == 0) atomicOr(a.err, kErrAttend);
       return ok;
     };
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
       const bool busy = (warp & 3) * 32 < x.live;  // a warp without rows only keeps the barriers' count
       float m = -INFINITY, l = 0.f;
       for (int s = s0 + t; s < s1; s += 2, ++cnt) {
-        if (!mb_wait(s_full + t, cnt & 1)) {
+        if (!mb_wait_warp(s_full + t, cnt & 1, a.wait_limit)) {
           if (lane == 0) atomicOr(a.err, kErrAttend);
           return false;
         }
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
       // ---- the piece's result: stream 0's threads join the two streams, row by row
       const bool two = s1 - s0 > 1;
       if (t == 0 || two) {
-        if (!mb_wait(o_full + t, n_o & 1)) {
+        if (!mb_wait_warp(o_full + t, n_o & 1, a.wait_limit)) {
           if (lane == 0) atomicOr(a.err, kErrAttend);
           return false;
         }

@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
           for (int part = 0; part < 2; ++part, ++g) {
             if constexpr (KV == 0) {
               const int st = g % ST;
-              if (g >= ST && !mb_wait(empty + st, ((g / ST) - 1) & 1)) {
+              if (g >= ST && !mb_wait_warp(empty + st, ((g / ST) - 1) & 1, a.wait_limit)) {
                 if (lane == 0) atomicOr(a.err, kErrAttend);
                 return false;
               }
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
                        ((my * 2 + part) * P.n_kv_heads + x.head) * 16, full + st);
             } else {
               const int r = g % RAW;
-              if (g >= RAW && !mb_wait(raw_empty + r, ((g / RAW) - 1) & 1)) {
+              if (g >= RAW && !mb_wait_warp(raw_empty + r, ((g / RAW) - 1) & 1, a.wait_limit)) {
                 if (lane == 0) atomicOr(a.err, kErrAttend);
                 return false;
               }
@@ -263,8 +263,8 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
       };
       for_share(a, sh, [&](const Unit& x, int, int s0, int s1) {
         const int nt = x.n_rows - x.r0 > kRows ? 2 : 1, n = s1 - s0;
-        bool ok = mb_wait(full + g % ST, (g / ST) & 1);
-        for (int t = 0; t < nt && ok; ++t) ok = mb_wait(q_full + t, pieces[t] & 1);
+        bool ok = mb_wait(full + g % ST, (g / ST) & 1, a.wait_limit);
+        for (int t = 0; t < nt && ok; ++t) ok = mb_wait(q_full + t, pieces[t] & 1, a.wait_limit);
         if (ok) {
           tc_after();
           for (int t = 0; t < nt; ++t) qk(t, g % ST);
@@ -272,9 +272,9 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
           for (int j = 0; j < n && ok; ++j) {
             const int gv = g + 1 + 2 * j, sv = gv % ST, sk = (gv + 1) % ST;
             const bool next = j + 1 < n;
-            ok = mb_wait(full + sv, (gv / ST) & 1);
+            ok = mb_wait(full + sv, (gv / ST) & 1, a.wait_limit);
             for (int t = 0; t < nt && ok; ++t) {
-              ok = mb_wait(p_full + t, (cnt[t] + j) & 1);
+              ok = mb_wait(p_full + t, (cnt[t] + j) & 1, a.wait_limit);
               if (!ok) break;
               tc_after();
               const uint64_t vd = smem_desc(ring_a + sv * C::kTile, C::kHalf);
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
                        (j | k) != 0);
               if (next) {
                 if (t == 0) {
-                  ok = mb_wait(full + sk, ((gv + 1) / ST) & 1);
+                  ok = mb_wait(full + sk, ((gv + 1) / ST) & 1, a.wait_limit);
                   if (!ok) break;
                   tc_after();
                 }
@@ -327,7 +327,8 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
           const int live = len - (x.key0 + s * kKeys);  // rows that hold tokens
           for (int part = 0; part < 2; ++part, ++g) {
             const int r = g % RAW, st = g % ST;
-            if (!mb_wait(raw_full + r, (g / RAW) & 1) || (g >= ST && !mb_wait(empty + st, ((g / ST) - 1) & 1))) {
+            if (!mb_wait_warp(raw_full + r, (g / RAW) & 1, a.wait_limit) ||
+                (g >= ST && !mb_wait_warp(empty + st, ((g / ST) - 1) & 1, a.wait_limit))) {
               if (lane == 0) atomicOr(a.err, kErrAttend);
               return false;
             }
@@ -411,7 +412,7 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
       const int t_hi = x.sg.pos0 + (min(x.r0 + t * kRows + kRows, x.n_rows) - 1) / G;
       float m = -INFINITY, l = 0.f;
       for (int s = s0; s < s1; ++s, ++cnt) {
-        if (!mb_wait(s_full + t, cnt & 1)) {
+        if (!mb_wait_warp(s_full + t, cnt & 1, a.wait_limit)) {
           if (lane == 0) atomicOr(a.err, kErrAttend);
           return false;
         }
@@ -479,7 +480,7 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
         if (lane == 0) mb_arrive(p_full + t);
       }
       // ---- the piece's result
-      if (!mb_wait(o_full + t, n_o & 1)) {
+      if (!mb_wait_warp(o_full + t, n_o & 1, a.wait_limit)) {
         if (lane == 0) atomicOr(a.err, kErrAttend);
         return false;
       }

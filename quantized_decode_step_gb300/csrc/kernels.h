@@ -328,6 +328,7 @@ struct AttendArgs {
   AttendSeg seg[MAG_MAX_BATCH];
   PoolGeom pool;
   uint32_t* err;
+  uint32_t wait_limit;  // polls of a pipeline wait before its role gives up (drains always use kWaitPolls)
 };
 // Block b takes the steps from (unit[b], step[b]) up to (unit[b + 1], step[b + 1]); no share is empty.
 constexpr int kAttendMaxShares = 160;

@@ -117,6 +117,7 @@ static mag_status run_attend(mag_ctx* c, int32_t layer, const KvRows& rows, cons
   a.scale_log2 = scale * 1.44269504088896340736f;
   a.pool = pool_geom(c);
   a.err = c->d_err;
+  a.wait_limit = c->wait_limit;
   const mag_status ws = attend_workspace(c);
   if (ws != MAG_OK) return ws;
   a.part = c->at_part;

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import quantized_decode_step_gb300 as mag
-from tests.test_gpu_ops import check, half, make, reference, sample_case
+from tests.test_gpu_ops import ALL_KV, KV_NAMES, check, half, make, reference, sample_case
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +59,51 @@ def test_calls_after_a_refused_allocation():
     refused()
     mag.quantize_w4g32(src, 64, 256, codes, sm)
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------------------------------------ waits that run out
+@pytest.mark.parametrize("kv", ALL_KV, ids=KV_NAMES.get)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new", [30, 200])
+@pytest.mark.parametrize("polls", [0, 1, 3])
+def test_attend_waits_give_up_then_context_recovers(kv, dim, new, polls):
+    """Every wait between the roles of the kernels for more than 16 packed rows gives up at its first poll (as if what it waits
+    for were stuck), or after one or three, where most waits end in time and some warps' do not: mag_sync says so, or
+    the result is right. With the limit restored the same call gives the bits that it gave before. The kernel for
+    fewer rows has no waits and works throughout."""
+    rng = np.random.default_rng(new)
+    n = 9000 + new
+    ctx = make(kv, 16, 8, dim, pool_blocks=n // 16 + 2, max_context=n)
+    sid = ctx.session_open()
+    k, v = half(rng, 1, n, 8, dim), half(rng, 1, n, 8, dim)
+    ctx.kv_append(sid, n, k.cuda(), v.cuda())
+    q = half(rng, new, 16, dim).cuda()
+    want, few = torch.empty_like(q), torch.empty_like(q[:1])
+    ctx.attend(0, [sid], [new], q, want)
+    ctx.attend(0, [sid], [1], q, few)
+    ctx.sync()
+    ctx.set_wait_limit(polls)
+    for _ in range(3):
+        out = torch.empty_like(q)
+        ctx.attend(0, [sid], [new], q, out)
+        if polls:
+            try:
+                ctx.sync()
+                assert torch.equal(out, want)
+            except mag.MagError as e:
+                assert e.status == mag.ERR_TIMEOUT and "gave up" in str(e)
+        else:
+            with pytest.raises(mag.MagError) as e:
+                ctx.sync()
+            assert e.value.status == mag.ERR_TIMEOUT and "gave up" in str(e.value)
+        ctx.sync()  # the error word was read and cleared
+        one = torch.empty_like(few)
+        ctx.attend(0, [sid], [1], q, one)
+        ctx.sync()
+        assert torch.equal(one, few)
+    ctx.set_wait_limit(-1)
+    for _ in range(2):
+        out = torch.empty_like(q)
+        ctx.attend(0, [sid], [new], q, out)
+        ctx.sync()
+        assert torch.equal(out, want)
