@@ -424,8 +424,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     for (int u = blockIdx.x, it = 0; u < n_units; u += gridDim.x, ++it) {
       const int ab = it & 1, nt = unit_tiles(u);
       const int n0 = unit_wt(u) * BN;
-      if (!mb_wait(acc_full + ab, (it >> 1) & 1, a.wait_limit)) {
-        atomicOr(a.err, 32u);
+      if (!__all_sync(0xffffffffu, mb_wait(acc_full + ab, (it >> 1) & 1, a.wait_limit))) {  // a warp leaves together
+        if (lane == 0) atomicOr(a.err, 32u);
         break;
       }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");

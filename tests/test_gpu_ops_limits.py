@@ -107,3 +107,34 @@ def test_attend_waits_give_up_then_context_recovers(kv, dim, new, polls):
         ctx.attend(0, [sid], [new], q, out)
         ctx.sync()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("polls", [0, 1, 3])
+def test_chunk_waits_give_up_then_context_recovers(polls):
+    """The same of the prefill GEMM's roles: a chunk times out or gives the bits that it gave before, and gives them
+    again with the limit restored."""
+    import synth
+    from synth import driver
+    from synth.workloads import TINY, Workload
+    wl = Workload("tiny-wait", TINY, mag.KV_FP16, 1, (128,), chunk=64)
+    ctx, sids = driver.setup(wl, 3, extra_tokens=60)
+    sid, p = sids[0], wl.prior[0]
+    x = torch.from_numpy(synth.hidden_f16(3, 48, TINY.hidden, tag="chunk")).cuda()
+
+    def chunk():
+        out = torch.empty(TINY.hidden, dtype=torch.float16, device="cuda")
+        ctx.session_truncate(sid, p)
+        ctx.prefill_chunk(sid, 48, x, out)
+        ctx.sync()
+        return out
+
+    want = chunk()
+    ctx.set_wait_limit(polls)
+    for _ in range(5):
+        try:
+            got = chunk()
+            assert polls and torch.equal(got, want)
+        except mag.MagError as e:
+            assert e.status == mag.ERR_TIMEOUT
+    ctx.set_wait_limit(-1)
+    assert torch.equal(chunk(), want) and torch.equal(chunk(), want)
