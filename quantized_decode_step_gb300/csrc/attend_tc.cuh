@@ -9,6 +9,20 @@ namespace tc {
 
 constexpr int kRows = 128, kKeys = 128;  // rows of a tile, keys of a step
 constexpr float kLazy = 8.0f, kShift = 7.0f;
+// A row's reference m is a score as the tensor core left it (-inf before the first that is seen), and
+// p = 2^(scale (v - m) + kShift). Of |scale m| up to kNear that is one multiply-add of v, its offset off by less than 2^-16.
+// Further from zero, where fp32 would round the scaled scores by up to more than the range of p, m is taken from v first
+// and is the largest score itself.
+constexpr float kNear = 256.0f;
+struct Reference {
+  float m, lazy;  // a score above m + lazy raises m
+  bool far;       // a row of the warp is further than kNear
+  __device__ __forceinline__ explicit Reference(float scale) : m(-INFINITY), lazy(by(scale)), far(false) {}
+  __device__ __forceinline__ static float by(float scale) { return fminf(kLazy / scale, 1e30f); }
+  // By a warp of which a row has to: every row's m to at least top; returns the factor of what was added up so far.
+  __device__ __forceinline__ float raise(float top, float scale);
+  __device__ __forceinline__ float value() const { return m == -INFINITY ? 0.f : m; }
+};
 constexpr uint32_t kErrAttend = 512u;
 
 __device__ __forceinline__ uint32_t su32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -124,6 +138,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+__device__ __forceinline__ float Reference::raise(float top, float scale) {
+  const float mn = fmaxf(m, top);
+  const float f = m == -INFINITY ? 0.f : ex2((m - mn) * scale);
+  m = mn;
+  const bool mine = fabsf(value()) * scale > kNear;
+  lazy = mine ? 0.f : by(scale);
+  far = __any_sync(0xffffffffu, mine);
+  return f;
 }
 struct F2 {
   unsigned long long v;

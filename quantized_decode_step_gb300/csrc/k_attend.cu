@@ -15,7 +15,7 @@
 // 2t+8, 2t+9 it reads the dimensions of column group g and pairs neighbouring rows with byte permutes.
 //
 // Softmax: base 2, the scores in fp32, a running maximum per row that is only raised when a score passes it by
-// more than 2^8 (p in fp16 is scaled by 2^7, so it stays below 65504, and 2^-21 of the maximum is still a normal
+// 2^8 or more (p in fp16 is scaled by 2^7, so it stays below 65504, and 2^-21 of the maximum is still a normal
 // number); the sum adds the rounded p, so that the weights of the sum in fp32 are those of the products. One
 // block per SM takes an equal share of all sessions' and heads' pool blocks, in order; a unit that is cut by the
 // end of a share leaves (m, l, o) in a workspace, and the last of its blocks to arrive adds the parts in order,
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(few_warps<D, KV, NT>() * 32, 1)
             if (back < 0 || (a.window && back >= a.window)) x = -INFINITY;
           }
           s[n][e] = x;
-          raise |= x > m[n][e & 1] + kLazy;
+          raise |= x >= m[n][e & 1] + kLazy;  // 2^26 and more from zero one step of fp32 is 8 or more
         }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll

@@ -1,6 +1,6 @@
 // The parts that the tcgen05 attention kernels leave of units whose keys went to several blocks, put together:
 //
-//   o = sum_b 2^(m_b - m) o_b / sum_b 2^(m_b - m) l_b,   m = max_b m_b,   in the blocks' order.
+//   o = sum_b 2^(scale (m_b - m)) o_b / sum_b 2^(scale (m_b - m)) l_b,   m = max_b m_b,   in the blocks' order.
 //
 // A part is [D values, m, l][128 rows] in fp32, column by column, as the kernels' threads, one row each, write it.
 // What bounds it: reading the parts from L2 (64 KB a tile and part), so it is a kernel of its own: the last block of a unit to
@@ -31,6 +31,7 @@ __global__ void __launch_bounds__(kWarps * 32) attend_merge_kernel(const __grid_
   if (r - lane >= sg.n_tok * a.group) return;
   const int b0 = cuts.first[cut], b1 = cuts.last[cut], slot0 = cuts.slot[cut];
   constexpr int kPart = (D + 2) * 128;
+  const float scale = fabsf(a.scale_log2) > 0.f ? fabsf(a.scale_log2) : 1.f;  // as the kernels take it
   auto part_of = [&](int b) {
     return a.part + (int64_t)((b == b0 ? slot0 : 2 * b) * tiles + tile) * kPart + row;
   };
@@ -57,7 +58,7 @@ __global__ void __launch_bounds__(kWarps * 32) attend_merge_kernel(const __grid_
     float mn = m;
 #pragma unroll
     for (int k = 0; k < GP; ++k) mn = fmaxf(mn, mb[k]);
-    const float f0 = m == -INFINITY ? 0.f : exp2f(m - mn);
+    const float f0 = m == -INFINITY ? 0.f : exp2f((m - mn) * scale);
     m = mn;
     l *= f0;
 #pragma unroll
@@ -65,7 +66,7 @@ __global__ void __launch_bounds__(kWarps * 32) attend_merge_kernel(const __grid_
 #pragma unroll
     for (int k = 0; k < GP; ++k) {
       if (mb[k] == -INFINITY) continue;  // nothing there (a part of masked keys, or past the last)
-      const float f = exp2f(mb[k] - m);
+      const float f = exp2f((mb[k] - m) * scale);
       l = fmaf(f, lb[k], l);
 #pragma unroll
       for (int i = 0; i < CW; ++i) o[i] = fmaf(f, v[k][i], o[i]);

@@ -445,7 +445,8 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
       const int r = x.r0 + row;
       const int pos = x.sg.pos0 + min(r, x.n_rows - 1) / G;
       const bool busy = (warp & 3) * 32 < x.live;  // a warp without rows only keeps the barriers' count
-      float m = -INFINITY, l = 0.f;
+      Reference ref(scale);
+      float l = 0.f;
       for (int s = s0 + t; s < s1; s += 2, ++cnt) {
         if (!mb_wait_warp(s_full + t, cnt & 1, a.wait_limit)) {
           if (lane == 0) atomicOr(a.err, kErrAttend);
@@ -475,11 +476,8 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
             for (int i = 2; i + 4 <= 32; i += 4) x0 = max3(x0, v[i], v[i + 1]), x1 = max3(x1, v[i + 2], v[i + 3]);
             top = max3(top, fmaxf(x0, x1), fmaxf(v[30], v[31]));
           }
-          top *= scale;
-          if (__any_sync(0xffffffffu, top > m + kLazy)) {
-            const float mn = fmaxf(m, top);
-            const float f = m == -INFINITY ? 0.f : ex2(m - mn);
-            m = mn;
+          if (__any_sync(0xffffffffu, top > ref.m + ref.lazy)) {
+            const float f = ref.raise(top, scale);
             l *= f;
             if (s > s0 + 1) {
 #pragma unroll 1
@@ -493,7 +491,7 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
               }
             }
           }
-          const float off = kShift - (m == -INFINITY ? 0.f : m);
+          const float off = ref.far ? kShift : kShift - ref.value() * scale;
           const F2 sc2 = f2(scale, scale), off2 = f2(off, off);
           F2 sum[2] = {f2(l, 0.f), f2(0.f, 0.f)};
           // P of columns c .. c + 31 goes over S's columns c / 2 .. c / 2 + 15, which are read by then
@@ -501,6 +499,10 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
           for (int c = 0; c < kKeys; c += 32) {
             float v[32];
             load(c, v);
+            if (ref.far) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] -= ref.value();
+            }
             uint32_t p[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -533,15 +535,16 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
         ++n_o;
       }
       tc_after();
-      if (t == 1) ml_b[row] = two ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+      if (t == 1) ml_b[row] = two ? make_float2(ref.m, l) : make_float2(-INFINITY, 0.f);
       if (!all()) return false;
       const bool whole = s0 == 0 && s1 == x.n_steps;
       const int mine = 2 * (int)blockIdx.x + (u == sh.unit[blockIdx.x] ? 0 : 1);
       constexpr int kPart = (D + 2) * kRows;  // as k_attend_merge.cu reads it
       if (t == 0 && busy) {
         const float2 b = ml_b[row];
-        const float mt = fmaxf(m, b.x);
-        const float fa = m == -INFINITY ? 0.f : ex2(m - mt), fb = b.x == -INFINITY ? 0.f : ex2(b.x - mt);
+        const float mt = fmaxf(ref.m, b.x);
+        const float fa = ref.m == -INFINITY ? 0.f : ex2((ref.m - mt) * scale);
+        const float fb = b.x == -INFINITY ? 0.f : ex2((b.x - mt) * scale);
         const float lt = fmaf(fb, b.y, fa * l), inv = 1.0f / lt;
         const bool live = row < x.live;
         __half* dst = a.o + (int64_t)(x.sg.row0 + r / G) * a.ldo + (int64_t)(x.head * G + r % G) * D;

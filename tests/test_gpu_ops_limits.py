@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import quantized_decode_step_gb300 as mag
-from tests.test_gpu_ops import ALL_KV, KV_NAMES, check, half, make, reference, sample_case
+from tests.test_gpu_ops import ALL_KV, KV_NAMES, as_stored, check, half, make, reference, sample_case
 
 pytestmark = pytest.mark.gpu
 
@@ -138,3 +138,73 @@ def test_chunk_waits_give_up_then_context_recovers(polls):
             assert e.status == mag.ERR_TIMEOUT
     ctx.set_wait_limit(-1)
     assert torch.equal(chunk(), want) and torch.equal(chunk(), want)
+
+
+# ------------------------------------------------------------------------------------------------ scores far from zero
+@pytest.mark.parametrize("kv", ALL_KV, ids=KV_NAMES.get)
+@pytest.mark.parametrize("scale", [128 ** -0.5, 1.0, -1.0], ids=["default", "one", "minus"])
+@pytest.mark.parametrize("prior,new", [(700, 2), (700, 30), (2500, 2), (2500, 30), (300, 200), (2500, 150)])
+def test_attend_scores_far_from_zero(kv, scale, prior, new):
+    """Scores of up to 2^37 that lie 2^20 and more apart, or are equal: a token's output is the mean of the values whose score is
+    its largest, to the rounding of the output and, of a mean of n, of weights 1 / n in fp16."""
+    rng = np.random.default_rng(prior + new)
+    n = prior + new
+    # constant key vectors: exact in an INT4 pool, and multiples of the same stored scale in an INT8 one
+    level = torch.from_numpy((rng.integers(-200, 201, n) * 128).astype(np.float16))
+    k = level.view(n, 1, 1).expand(n, 2, 128).contiguous()
+    v, q = half(rng, n, 2, 128), torch.full((new, 4, 128), 2.0 ** 15, dtype=torch.float16)
+    q[1::2] = -2.0 ** 15
+    ctx = make(kv, 4, 2, 128, pool_blocks=n // 16 + 2, max_context=n)
+    sid = ctx.session_open()
+    ctx.session_extend([sid], [n])
+    ctx.kv_write(0, [sid], [n], k.cuda(), v.cuda())
+    out = torch.empty((new, 4, 128), dtype=torch.float16, device="cuda")
+    ctx.attend(0, [sid], [new], q.cuda(), out, scale=scale)
+    ctx.sync()
+    check(out, *reference(q, as_stored(k, kv), as_stored(v, kv), prior, 0, scale), 2)
+
+
+@pytest.mark.parametrize("shift", range(20, 36))
+@pytest.mark.parametrize("new", [1, 20, 130])
+def test_attend_rising_scores_of_any_size(new, shift):
+    """Scores around 2^shift that rise by steps of fp32, so that they pass the running maximum by less than, about, and more
+    than what they may: the output is a mean of its keys' values, 1 and 3."""
+    n, dims = 1000 + new, 1 << max(0, shift - 30)
+    a = min(15, shift // 2)
+    k, q = torch.zeros((n, 1, 64), dtype=torch.float16), torch.zeros((new, 1, 64), dtype=torch.float16)
+    k[..., :dims], q[..., :dims] = 2.0 ** a, 2.0 ** min(15, shift - a)
+    k[:, 0, 63], q[..., 63] = (torch.arange(n) % 1024).half(), 2.0 ** (shift - 23)
+    v = torch.ones((n, 1, 64), dtype=torch.float16)
+    v[::2] = 3.0
+    ctx = make(mag.KV_FP16, 1, 1, 64, pool_blocks=n // 16 + 2, max_context=n)
+    sid = ctx.session_open()
+    ctx.session_extend([sid], [n])
+    ctx.kv_write(0, [sid], [n], k.cuda(), v.cuda())
+    out = torch.empty((new, 1, 64), dtype=torch.float16, device="cuda")
+    ctx.attend(0, [sid], [new], q.cuda(), out, scale=1.0)
+    ctx.sync()
+    # half a step of fp16 at 3 is 2^-10; the weights' roundings move a mean of 1 and 3 no further than they differ
+    assert torch.isfinite(out).all() and (out >= 1 - 2.0 ** -10).all() and (out <= 3 + 2.0 ** -8).all(), out.unique()
+
+
+@pytest.mark.parametrize("new", [1, 20, 130])
+def test_attend_scores_that_pass_the_maximum_by_just_what_they_may(new):
+    """Around 2^26, where steps of fp32 are as large as what a score may pass the running maximum by before it is raised: two
+    scores one step apart, in turn along the keys, from eight starts (the scaled step is 8 or 16)."""
+    n = 100000 + new
+    k, q = torch.zeros((n, 1, 64), dtype=torch.float16), torch.zeros((new, 1, 64), dtype=torch.float16)
+    k[..., 0], q[..., 0] = 2.0 ** 11, 2.0 ** 15
+    k[:, 0, 1], q[..., 1] = ((torch.arange(n) // 256) % 2).half(), 8.0
+    k[..., 2] = 1.0
+    v = torch.ones((n, 1, 64), dtype=torch.float16)
+    v[::2] = 3.0
+    ctx = make(mag.KV_FP16, 1, 1, 64, pool_blocks=n // 16 + 2, max_context=n)
+    sid = ctx.session_open()
+    ctx.session_extend([sid], [n])
+    ctx.kv_write(0, [sid], [n], k.cuda(), v.cuda())
+    for start in range(8):
+        q[..., 2] = 8.0 * start
+        out = torch.empty((new, 1, 64), dtype=torch.float16, device="cuda")
+        ctx.attend(0, [sid], [new], q.cuda(), out, scale=1.0)
+        ctx.sync()
+        assert torch.isfinite(out).all() and (out >= 1 - 2.0 ** -10).all() and (out <= 3 + 2.0 ** -8).all(), start
