@@ -325,8 +325,8 @@ typedef struct mag_sample_params {
  *   token is the first whose running sum of w exceeds u times the prefix's sum.
  * Sums are exact in integers (w in units of 2^-40), so a result depends on nothing but its row. token_dev[row] is
  * the token's index, -1 for a row with no token to draw (none allowed, or every logit NaN or -inf; those are never
- * drawn); prob_dev[row] (may be null) its share of the kept w, NaN for a row without a token. Infinite
- * logits share all the weight. A uniform number below 0 or NaN counts as 0, one of 1 or more takes the prefix's last
+ * drawn); prob_dev[row] (may be null) its share of the kept w, to 2^-23 of itself however small, NaN for a row without a
+ * token. Infinite logits share all the weight. A uniform number below 0 or NaN counts as 0, one of 1 or more takes the prefix's last
  * token. p may be null (temperature 1, no cuts). Arrays are aligned to their elements.
  * Errors: INVALID_ARG, UNSUPPORTED (vocab above 540,672 in fp16, 270,336 in fp32), CUDA. */
 mag_status mag_sample(const void* logits_dev, int32_t logits_type, int32_t rows, int32_t vocab, int64_t ld,

@@ -78,6 +78,14 @@ __device__ __forceinline__ float value_of(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
+// w / total to one rounding: both as two fp32 terms, the quotient corrected by its remainder.
+__device__ float quotient(u64 w, u64 total) {
+  const float wh = __ull2float_rn(w), wl = __ll2float_rn((long long)(w - __float2ull_rn(wh)));
+  const float th = __ull2float_rn(total), tl = __ll2float_rn((long long)(total - __float2ull_rn(th)));
+  const float q = wh / th;
+  return q + (fmaf(-q, th, wh) + fmaf(-q, tl, wl)) / th;
+}
+
 // exp((x - max) / T) in units of 2^-40, of t = (max - x) (kh + kl) below kMaxT; kh + kl = log2(e) / T. Without a branch, so
 // that several tokens' run side by side.
 constexpr float kDeadT = 41.99f;   // t of a token that cannot be drawn; it weighs 0
@@ -119,6 +127,15 @@ struct Weight {
     int bits;
     split<kExact>(x, t(x), m, bits);
     return any(m, bits);
+  }
+  // The weight over total, before the weight's rounding to units: that would leave a token of 2^-28 of the largest one's
+  // weight a probability of 12 bits.
+  template <bool kExact>
+  __device__ float share(float x, u64 total) const {
+    uint32_t m;
+    int bits;
+    split<kExact>(x, t(x), m, bits);
+    return ldexpf(quotient(m, total), 9 - (((bits - kMagicBits) >> 8) + 10));
   }
 };
 
@@ -170,15 +187,6 @@ __device__ u64 beyond(float u, u64 total) {  // smallest sum above u times total
   if (u >= 1.f) return total;
   bool more;
   return min(total, times(u, total, more) + 1);
-}
-
-
-// w / total to one rounding: both as two fp32 terms, the quotient corrected by its remainder.
-__device__ float quotient(u64 w, u64 total) {
-  const float wh = __ull2float_rn(w), wl = __ll2float_rn((long long)(w - __float2ull_rn(wh)));
-  const float th = __ull2float_rn(total), tl = __ll2float_rn((long long)(total - __float2ull_rn(th)));
-  const float q = wh / th;
-  return q + (fmaf(-q, th, wh) + fmaf(-q, tl, wl)) / th;
 }
 
 // The settings of a row.
@@ -755,7 +763,7 @@ class Sampler {
   }
   __device__ void write(int32_t index, uint32_t key, u64 total) {
     a_.token[row_] = index;
-    if (a_.prob) a_.prob[row_] = quotient(weight(value_of(key)), total);
+    if (a_.prob) a_.prob[row_] = w_.template share<kExact>(value_of(key), total);
   }
 
   __device__ void draw(int k, bool use_p, float top_p, bool use_m, u64 least, float u) {
@@ -977,8 +985,8 @@ class CountedRow {
     __syncthreads();
     const bool none = !(mx > -INFINITY);
     if (none || g.greedy) {
-      if (!none) locate(__half_as_ushort(__float2half_rn(mx)), 1, 1, 1);
-      else if (tid_ == 0) write(-1, 1, 0);
+      if (!none) locate(__half_as_ushort(__float2half_rn(mx)), 1, 0);
+      else if (tid_ == 0) write(-1, 0, 0);
       return true;
     }
     infinite_ = mx == INFINITY;  // infinite logits share all the weight
@@ -1010,7 +1018,7 @@ class CountedRow {
       __syncthreads();
     }
     const Place p = find(false, beyond(g.u, total));
-    locate(p.index, p.tie, weight(p.index), total);
+    locate(p.index, p.tie, total);
     return true;
   }
 
@@ -1241,8 +1249,8 @@ class CountedRow {
     return (p & 0x8000u) ? (int)(p >> 6) - 15 : 496 - (int)(p >> 6);
   }
 
-  // Writes the tie-th token (from 1) of a pattern, by tiles of 1,024 threads' runs.
-  __device__ void locate(uint32_t pattern, uint32_t tie, u64 w, u64 total) {
+  // Writes the tie-th token (from 1) of a pattern, found by tiles of 256 tokens.
+  __device__ void locate(uint32_t pattern, uint32_t tie, u64 total) {
     // a warp's run of 256 tokens is a tile; their tokens of the pattern
     const int n_tiles = (a_.vocab + 255) / 256;
     for (int i = tid_; i < kCountThreads; i += kCountThreads) sm_.tiles[i] = 0;
@@ -1285,13 +1293,17 @@ class CountedRow {
       uint32_t left = sm_.tie - (c - own);  // the wanted one's number among the lane's, if it is there
       if (c - own < sm_.tie && sm_.tie <= c) {
         while (--left) m &= m - 1;
-        write(i0 + __ffs(m) - 1, w, total);
+        write(i0 + __ffs(m) - 1, pattern, total);
       }
     }
   }
-  __device__ void write(int32_t index, u64 w, u64 total) {
+  // total 0: the first largest logit, for itself
+  __device__ void write(int32_t index, uint32_t pattern, u64 total) {
     a_.token[row_] = index;
-    if (a_.prob) a_.prob[row_] = index < 0 ? __int_as_float(0x7fc00000) : quotient(w, total);
+    if (!a_.prob) return;
+    if (index < 0) a_.prob[row_] = __int_as_float(0x7fc00000);
+    else if (total == 0) a_.prob[row_] = 1.0f;
+    else a_.prob[row_] = w_.template share<false>(infinite_ ? 0.f : __half2float(__ushort_as_half((uint16_t)pattern)), total);
   }
 
   const SampleArgs& a_;

@@ -208,3 +208,28 @@ def test_attend_scores_that_pass_the_maximum_by_just_what_they_may(new):
         ctx.attend(0, [sid], [new], q.cuda(), out, scale=1.0)
         ctx.sync()
         assert torch.isfinite(out).all() and (out >= 1 - 2.0 ** -10).all() and (out <= 3 + 2.0 ** -8).all(), start
+
+
+# ------------------------------------------------------------------------------------------------ small probabilities
+@pytest.mark.parametrize("dtype", [np.float16, np.float32])
+@pytest.mark.parametrize("rows,vocab", [(1, 50), (3, 20000), (30, 300), (30, 40000), (160, 300)])
+@pytest.mark.parametrize("k", [0, 5, 2000])
+def test_sample_probability_of_an_unlikely_token(dtype, rows, vocab, k):
+    """Four tokens down to 2^-38 of the largest one's weight, the last of them drawn (u = 1): its probability is good to
+    2^-24, the rounding of the quotient, and what the weights are good to, 2^-28, of itself."""
+    rng = np.random.default_rng(vocab)
+    x = np.full((rows, vocab), -np.inf, dtype)
+    far = rng.uniform(10.0, 26.0, rows).astype(dtype)
+    for r in range(rows):
+        at = rng.permutation(vocab)[:4]
+        x[r, at] = np.array([0.0, -1.5, -4.25, -far[r]], dtype)
+    token = torch.full((rows,), -7, dtype=torch.int32, device="cuda")
+    prob = torch.empty(rows, dtype=torch.float32, device="cuda")
+    mag.sample(torch.from_numpy(x).cuda(), rows, vocab, torch.ones(rows, device="cuda"), token, prob=prob,
+               dtype=mag.LOGITS_F16 if dtype == np.float16 else mag.LOGITS_F32,
+               top_k=torch.full((rows,), k, dtype=torch.int32, device="cuda") if k else None)
+    torch.cuda.synchronize()
+    w = np.exp(np.where(np.isfinite(x), x, -np.inf).astype(np.float64))
+    for r, (t, p) in enumerate(zip(token.cpu().tolist(), prob.cpu().tolist())):
+        assert x[r, t] == -far[r]
+        assert abs(p / (w[r, t] / w[r].sum()) - 1) <= 2.0 ** -24 + 2.0 ** -28, (r, p, w[r, t] / w[r].sum())
