@@ -296,7 +296,10 @@ mag_status mag_kv_export(mag_ctx* ctx, int32_t session, int32_t first, int32_t n
  * over the keys j <= p of a token at position p, and j > p - window when window > 0 (0: no window); k and v are the
  * fp16 values that mag_kv_read gives. q_dev is fp16 [rows][n_heads][head_dim] (already rotated), row stride ldq;
  * out_dev the same with row stride ldo; the two must not overlap. The sums, the softmax and its maximum are kept in
- * fp32. A row's result does not depend on the other sessions of the call beyond how its keys are split over blocks.
+ * fp32; for the products with v its weights are rounded to fp16 (2^-11 of a weight, 2^-32 of the row's largest). Sessions of
+ * up to 128 packed rows (tokens times n_heads / n_kv_heads) divide by the sum of the rounded weights, longer chunks by that of
+ * the weights before the rounding: values that are all equal come back as they are from the one, to 2^-11 of themselves
+ * from the other. A row's result does not depend on the other sessions of the call beyond how its keys are split over blocks.
  * The sessions' stored keys and values must be finite, those outside the window too (the product of 0 and an infinite
  * value is NaN); slots past a session's end may hold anything. scale must be finite.
  * Errors: INVALID_ARG (also a context's first call in a capture), OOM (the workspace), CUDA. */

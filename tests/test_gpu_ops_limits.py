@@ -233,3 +233,56 @@ def test_sample_probability_of_an_unlikely_token(dtype, rows, vocab, k):
     for r, (t, p) in enumerate(zip(token.cpu().tolist(), prob.cpu().tolist())):
         assert x[r, t] == -far[r]
         assert abs(p / (w[r, t] / w[r].sum()) - 1) <= 2.0 ** -24 + 2.0 ** -28, (r, p, w[r, t] / w[r].sum())
+
+
+# ------------------------------------------------------------------------------------------------ the sum of the weights
+@pytest.mark.parametrize("kv", ALL_KV, ids=KV_NAMES.get)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new", [1, 30, 200, 300])
+def test_attend_equal_values_come_back(kv, dim, new):
+    """Every value 1: the output is 1 whatever the weights, if their sum adds what the products take, which it does up to 128
+    packed rows. One key in 16 has the largest weight, the others half of it times 1 + 0.95 2^-11, which fp16 rounds
+    down by almost half a step; the sum of the weights before that rounding, by which longer chunks divide, is 0.84 2^-11
+    larger, and the output then the number below 1, or 1."""
+    n = 1500 + new
+    k, v = torch.ones((n, 1, dim), dtype=torch.float16), torch.ones((n, 1, dim), dtype=torch.float16)
+    k[::16] = 0
+    one = float(as_stored(v, kv)[0, 0, 0])
+    want = math.log(0.5 * (1 + 0.95 * 2.0 ** -11)) / one
+    q = torch.zeros((new, 2, dim), dtype=torch.float16)
+    q[..., 0] = want
+    q[..., 1] = want - float(np.float16(want))  # the two together: want to 2^-25
+    ctx = make(kv, 2, 1, dim, pool_blocks=n // 16 + 2, max_context=n)
+    sid = ctx.session_open()
+    ctx.session_extend([sid], [n])
+    ctx.kv_write(0, [sid], [n], k.cuda(), v.cuda())
+    out = torch.empty((new, 2, dim), dtype=torch.float16, device="cuda")
+    ctx.attend(0, [sid], [new], q.cuda(), out, scale=1.0)
+    ctx.sync()
+    if 2 * new <= 128:
+        assert (out.cpu() == one).all(), out.unique()
+    else:  # and half a step for the output's own rounding
+        assert ((out.cpu().double() - one).abs() <= one * 2.0 ** -10).all(), out.unique()
+
+
+@pytest.mark.parametrize("kv", ALL_KV, ids=KV_NAMES.get)
+@pytest.mark.parametrize("dim,group,new", [(64, 1, 17), (128, 4, 5), (64, 8, 16), (128, 2, 60), (128, 1, 128)])
+@pytest.mark.parametrize("prior", [40, 2300])
+def test_attend_up_to_128_rows_to_the_weights_rounding(kv, dim, group, new, prior):
+    """Sums of the rounded weights: with weights w_j (1 + e_j), |e_j| <= 2^-11, in both the products and the sum, o moves by at most
+    2^-11 sum_j w_j |v_j - o|, and its own rounding adds 2^-11 |o|; a tenth of that for fp32's part, and half of fp16's smallest
+    step twice."""
+    rng = np.random.default_rng(prior + new)
+    n = prior + new
+    k, v, q = half(rng, n, 2, dim), half(rng, n, 2, dim), half(rng, new, 2 * group, dim)
+    v[..., ::3] += 4.0  # an o that is large next to what the values differ by
+    ctx = make(kv, 2 * group, 2, dim, pool_blocks=n // 16 + 2, max_context=n)
+    sid = ctx.session_open()
+    ctx.session_extend([sid], [n])
+    ctx.kv_write(0, [sid], [n], k.cuda(), v.cuda())
+    out = torch.empty((new, 2 * group, dim), dtype=torch.float16, device="cuda")
+    ctx.attend(0, [sid], [new], q.cuda(), out)
+    ctx.sync()
+    o, spread = reference(q, as_stored(k, kv), as_stored(v, kv), prior, 0, dim ** -0.5)
+    tol = 1.1 * 2.0 ** -11 * (o.abs() + spread) + 2.0 ** -24
+    assert ((out.double().cpu() - o).abs() <= tol).all()
