@@ -301,7 +301,8 @@ mag_status mag_kv_export(mag_ctx* ctx, int32_t session, int32_t first, int32_t n
  * the weights before the rounding: values that are all equal come back as they are from the one, to 2^-11 of themselves
  * from the other. A row's result does not depend on the other sessions of the call beyond how its keys are split over blocks.
  * The sessions' stored keys and values must be finite, those outside the window too (the product of 0 and an infinite
- * value is NaN); slots past a session's end may hold anything. scale must be finite.
+ * value is NaN); slots past a session's end may hold anything. scale must be finite, and below 2.3e38; so must
+ * every scaled score be.
  * Errors: INVALID_ARG (also a context's first call in a capture), OOM (the workspace), CUDA. */
 mag_status mag_attend(mag_ctx* ctx, int32_t layer, int32_t n_sessions, const int32_t* session_ids_host,
                       const int32_t* n_tokens_host, const void* q_dev, int64_t ldq, void* out_dev, int64_t ldo,

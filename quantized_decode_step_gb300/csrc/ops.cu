@@ -101,6 +101,7 @@ static mag_status attend_workspace(mag_ctx* c) {
 // 59), up to kStreamRows (one tile) to the streaming one (20 rows over 20,000 FP16 keys: 30 us for the register
 // kernel's 68), others to the two-tile one. A pool too large for a tensor map's rows goes to the register kernel whole.
 constexpr int kFewRows = 16, kStreamRows = 128;
+constexpr float kLog2e = 1.44269504088896340736f;
 
 static mag_status run_attend(mag_ctx* c, int32_t layer, const KvRows& rows, const void* q, int64_t ldq, void* out, int64_t ldo,
                       int32_t window, float scale) {
@@ -114,7 +115,7 @@ static mag_status run_attend(mag_ctx* c, int32_t layer, const KvRows& rows, cons
   a.group = c->G;
   a.layer = layer;
   a.window = window;
-  a.scale_log2 = scale * 1.44269504088896340736f;
+  a.scale_log2 = scale * kLog2e;
   a.pool = pool_geom(c);
   a.err = c->d_err;
   a.wait_limit = c->wait_limit;
@@ -257,7 +258,7 @@ mag_status mag_attend(mag_ctx* c, int32_t layer, int32_t n, const int32_t* sids,
   mag_status st = op_rows(c, "attend", layer, n, sids, ntok, rows);
   if (st != MAG_OK) return st;
   if (window < 0) return fail(c, MAG_ERR_INVALID_ARG, "attend: window %d", window);
-  if (!std::isfinite(scale)) return fail(c, MAG_ERR_INVALID_ARG, "attend: the scale is not finite");
+  if (!std::isfinite(scale * kLog2e)) return fail(c, MAG_ERR_INVALID_ARG, "attend: the scale, or its log2(e)-fold, is not finite");
   if (rows.n_rows == 0) return MAG_OK;
   if ((st = op_buffer(c, "attend", "q", q, ldq, (int64_t)c->Hq * c->d)) != MAG_OK) return st;
   if ((st = op_buffer(c, "attend", "out", out, ldo, (int64_t)c->Hq * c->d)) != MAG_OK) return st;

@@ -286,3 +286,21 @@ def test_attend_up_to_128_rows_to_the_weights_rounding(kv, dim, group, new, prio
     o, spread = reference(q, as_stored(k, kv), as_stored(v, kv), prior, 0, dim ** -0.5)
     tol = 1.1 * 2.0 ** -11 * (o.abs() + spread) + 2.0 ** -24
     assert ((out.double().cpu() - o).abs() <= tol).all()
+
+
+def test_attend_refuses_a_scale_whose_base_2_form_overflows():
+    """Scores are taken in powers of two: a finite scale of which log2(e) times is not gave NaN."""
+    ctx = make(mag.KV_FP16, 4, 2, 64)
+    sid = ctx.session_open()
+    ctx.session_extend([sid], [20])
+    k, q = torch.zeros((20, 2, 64), device="cuda").half(), torch.zeros((20, 4, 64), device="cuda").half()
+    ctx.kv_write(0, [sid], [20], k, k + 1)
+    out = torch.zeros_like(q)
+    for scale in (2.5e38, -3.4e38):
+        with pytest.raises(mag.MagError) as e:
+            ctx.attend(0, [sid], [20], q, out, scale=scale)
+        assert e.value.status == mag.ERR_INVALID_ARG
+    for new in (1, 20):
+        ctx.attend(0, [sid], [new], q, out[:new], scale=2.3e38)
+        ctx.sync()
+        assert (out[:new] == 1).all()
