@@ -53,11 +53,11 @@ __device__ __forceinline__ bool mb_wait(uint64_t* b, uint32_t par, uint32_t limi
 __device__ __forceinline__ bool mb_wait_warp(uint64_t* b, uint32_t par, uint32_t limit) {
   return __all_sync(0xffffffffu, mb_wait(b, par, limit));
 }
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
           "r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(su32(bar))
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(su32(bar))
       : "memory");
 }
 __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -184,7 +184,8 @@ __device__ __forceinline__ bool join(uint64_t* bar, int& phase, uint32_t limit) 
   return mb_wait_warp(bar, phase++ & 1, limit);
 }
 
-// The tensor map of one layer's FP16 pool: rows of D values, [block][K, V][head][16], boxes of 16 rows and 64 values.
+// The tensor map of one layer's FP16 pool: [block][K, V; head; 16][D], boxes of 16 rows and 64 values. The blocks are a
+// dimension of their own, so that no coordinate passes 32 bits in any pool.
 inline cudaError_t pool_map(CUtensorMap* map, const AttendArgs& a) {
   typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                     const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -199,11 +200,11 @@ inline cudaError_t pool_map(CUtensorMap* map, const AttendArgs& a) {
   }();
   if (!fn) return cudaErrorNotSupported;
   const int d = a.pool.head_dim;
-  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)a.pool.pool_blocks * 2 * a.pool.n_kv_heads * 16};
-  cuuint64_t strides[1] = {(cuuint64_t)d * 2};
-  cuuint32_t box[2] = {64, 16}, es[2] = {1, 1};
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)2 * a.pool.n_kv_heads * 16, (cuuint64_t)a.pool.pool_blocks};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)a.pool.block_bytes};
+  cuuint32_t box[3] = {64, 16, 1}, es[3] = {1, 1, 1};
   void* base = a.pool.base + (int64_t)a.layer * a.pool.pool_blocks * a.pool.block_bytes;
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? cudaSuccess

@@ -130,8 +130,7 @@ struct Ring : RingShape<D, KV> {
         __syncwarp();
         const int blk = lane & 7, half = lane >> 3;
         if (blk < n_tma && half < D / 64)
-          tma_2d(su32(tile) + half * S::kHalf + blk * 2048, &map, half * 64, ((my * 2 + part) * P.n_kv_heads + head) * 16,
-                 full + st);
+          tma_3d(su32(tile) + half * S::kHalf + blk * 2048, &map, half * 64, (part * P.n_kv_heads + head) * 16, my, full + st);
         ++g;
         return true;
       });

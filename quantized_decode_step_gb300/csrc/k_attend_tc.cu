@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(Cfg<D, KV>::kThreads, 1)
               __syncwarp();
               const int blk = lane & 7, half = lane >> 3;
               if (blk < n_tma && half < D / 64)
-                tma_2d(dst + half * C::kHalf + blk * 2048, &map, half * 64,
-                       ((my * 2 + part) * P.n_kv_heads + x.head) * 16, full + st);
+                tma_3d(dst + half * C::kHalf + blk * 2048, &map, half * 64, (part * P.n_kv_heads + x.head) * 16, my,
+                       full + st);
             } else {
               const int r = g % RAW;
               if (g >= RAW && !mb_wait_warp(raw_empty + r, ((g / RAW) - 1) & 1, a.wait_limit)) {
@@ -577,11 +577,6 @@ cudaError_t launch_tc_kv(const Launch& L, const AttendArgs& a, const AttendShare
 }
 
 }  // namespace
-
-bool attend_tc_fits(const AttendArgs& a) {
-  // rows of the tensor map are 32-bit signed coordinates
-  return a.pool.pool_blocks * 2 * a.pool.n_kv_heads * 16 < (int64_t)1 << 31;
-}
 
 cudaError_t launch_attend_tc(const Launch& L, AttendArgs& a, int n_sm) {
   if (a.n_seg < 1 || a.n_seg > MAG_MAX_BATCH) return cudaErrorInvalidValue;

@@ -365,8 +365,7 @@ constexpr size_t kAttendArrivals = kAttendMaxShares;
 cudaError_t launch_attend_few(const Launch& L, AttendArgs& a, int n_sm, int tile_rows);
 // Up to 128 rows (tcgen05).
 cudaError_t launch_attend_stream(const Launch& L, AttendArgs& a, int n_sm);
-// Many rows (tcgen05); false where the pool is too large for it.
-bool attend_tc_fits(const AttendArgs& a);
+// Many rows (tcgen05).
 cudaError_t launch_attend_tc(const Launch& L, AttendArgs& a, int n_sm);
 
 // ---------------------------------------------------------------- sampling

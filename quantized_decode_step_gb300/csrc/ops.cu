@@ -99,7 +99,7 @@ static mag_status attend_workspace(mag_ctx* c) {
 // Which kernel a session goes to, by its packed rows (tokens times query heads per KV head): up to kFewRows to the
 // register kernel (one of its tiles; with the streaming kernel 16 sessions' single tokens over INT8 keys take 156 us for
 // 59), up to kStreamRows (one tile) to the streaming one (20 rows over 20,000 FP16 keys: 30 us for the register
-// kernel's 68), others to the two-tile one. A pool too large for a tensor map's rows goes to the register kernel whole.
+// kernel's 68), others to the two-tile one.
 constexpr int kFewRows = 16, kStreamRows = 128;
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -125,14 +125,13 @@ static mag_status run_attend(mag_ctx* c, int32_t layer, const KvRows& rows, cons
   a.part_ml = c->at_ml;
   a.arrivals = c->at_arrivals;
   const Launch L{c->stream, false, nullptr};
-  const int few_rows = attend_tc_fits(a) ? kFewRows : INT32_MAX;
   for (int kind = 0; kind < 3; ++kind) {
     int64_t most = 0;
     a.n_seg = 0;
     for (int i = 0; i < rows.n_seg; ++i) {
       const KvSeg& s = rows.seg[i];
       const int64_t n = (int64_t)s.n_tok * c->G;
-      if ((n <= few_rows ? 0 : (n <= kStreamRows ? 1 : 2)) != kind) continue;
+      if ((n <= kFewRows ? 0 : (n <= kStreamRows ? 1 : 2)) != kind) continue;
       a.seg[a.n_seg++] = AttendSeg{s.row0, s.n_tok, s.pos0, s.sess, 0, 0};
       most = std::max(most, n);
     }
