@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import quantized_decode_step_gb300 as mag
-from tests.test_gpu_ops import ALL_KV, KV_NAMES, as_stored, check, half, make, reference, sample_case
+from tests.test_gpu_ops import ALL_KV, KV_NAMES, as_stored, check, half, make, reference, rows_of, sample_case
 
 pytestmark = pytest.mark.gpu
 
@@ -304,3 +304,63 @@ def test_attend_refuses_a_scale_whose_base_2_form_overflows():
         ctx.attend(0, [sid], [new], q, out[:new], scale=2.3e38)
         ctx.sync()
         assert (out[:new] == 1).all()
+
+
+# ------------------------------------------------------------------------------------------------ sizes between the other tests'
+@pytest.mark.parametrize("kv", ALL_KV, ids=KV_NAMES.get)
+@pytest.mark.parametrize("kv_heads,dim", [(1, 64), (3, 128), (8, 128)])
+@pytest.mark.parametrize("lens,new", [((300, 1, 258, 2, 7, 900), (299, 1, 5, 2, 3, 721)), ((517,), (513,)),
+                                      ((130, 131, 129, 133), (130, 129, 127, 128))])
+def test_write_of_many_rows_of_several_sessions(kv, kv_heads, dim, lens, new):
+    """More than 512 rows, where a block of the kernel takes four neighbouring rows, of two sessions or the last ones: what is
+    read back equals the oracle's quantisers', older tokens stay."""
+    rng = np.random.default_rng(sum(new))
+    ctx = make(kv, kv_heads, kv_heads, dim, pool_blocks=sum(-(-n // 16) for n in lens) + 1, sessions=len(lens),
+               max_context=max(lens))
+    sids, ks, vs = [ctx.session_open() for _ in lens], [], []
+    for sid, n in zip(sids, lens):
+        k, v = half(rng, n, kv_heads, dim, std=2), half(rng, n, kv_heads, dim)
+        ctx.kv_append(sid, n, k.cuda(), v.cuda())
+        ctx.sync()
+        ks.append(k)
+        vs.append(v)
+    rows, width = sum(new), kv_heads * dim
+    nk, nv = half(rng, rows, kv_heads, dim), half(rng, rows, kv_heads, dim, std=3)
+    wide = torch.zeros((2, rows, width + 8), dtype=torch.float16, device="cuda")
+    wide[0, :, :width], wide[1, :, :width] = nk.view(rows, -1).cuda(), nv.view(rows, -1).cuda()
+    ctx.kv_write(0, sids, new, wide[0], wide[1], ld=width + 8)
+    at = 0
+    for sid, n, m, k, v in zip(sids, lens, new, ks, vs):
+        out = torch.empty((2, n, kv_heads, dim), dtype=torch.float16, device="cuda")
+        ctx.kv_read(0, [sid], [n], out[0], out[1])
+        ctx.sync()
+        for got, old, fresh in ((out[0], k, nk), (out[1], v, nv)):
+            assert torch.equal(got.cpu(), as_stored(torch.cat((old[:n - m], fresh[at:at + m])), kv))
+        at += m
+
+
+@pytest.mark.parametrize("dtype,rows,vocab", [(np.float32, 152, 128256), (np.float32, 153, 131071), (np.float32, 160, 131072),
+                                              (np.float16, 153, 131071), (np.float16, 20, 131072), (np.float16, 2, 540672),
+                                              (np.float32, 2, 270336), (np.float32, 9, 131072)])
+def test_sample_largest_rows(dtype, rows, vocab):
+    """Rows of a real vocabulary in the kernels for many rows, next to the border between kernels, and the largest that are
+    taken: whole distributions, equal logits (the largest sums), and cuts."""
+    rng = np.random.default_rng(vocab)
+    x = rows_of(rng, rows, vocab, dtype)
+    x[1::3] = dtype(0.5)
+    x[2::3] *= dtype(0.01)
+    sample_case(x, t=1.5, seed=1)
+    sample_case(x, t=0.7, p=0.95, seed=2)
+    sample_case(x, t=rng.uniform(0.3, 2, rows), k=rng.integers(0, vocab + 2, rows), p=rng.uniform(0, 1.1, rows),
+                m=rng.uniform(-0.1, 0.5, rows), seed=3)
+
+
+def test_sample_bins_as_wide_as_their_adds_allow():
+    """131,071 equal fp32 logits just below the largest, many rows: one bin takes all their weights, whose limbs of 15 bits are
+    nearly full."""
+    x = np.full((152, 131071), np.float32(-2.0 ** -20), np.float32)
+    x[:, 100] = 0.0
+    u = (np.arange(152) + 0.5) / 152
+    sample_case(x, u=u)
+    sample_case(x, p=0.5, u=u)
+    sample_case(x, k=131070, u=u)
