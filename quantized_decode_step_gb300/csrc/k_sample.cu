@@ -20,8 +20,8 @@
 // What bounds it: the logits are read once from HBM (256 rows of 128,256 in fp16: 10 us), so with few rows the
 // latency of the passes between cluster barriers, with many the instructions and shared-memory adds of a token:
 // about 7 and 1 to count it, 30 and 2 or 3 for its weight. With few rows a cluster of blocks shares a row, each
-// with its slice in shared memory, as many blocks as the row count leaves SMs for; with many a block has a row, two
-// blocks an SM, and later passes read it from L2.
+// with its slice in shared memory, as many blocks as the row count leaves SMs for; with many a block has a row and later
+// passes read it from L2: two blocks an SM, or one where long fp16 rows are counted by value (132 KB of counts).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -943,6 +943,7 @@ class Sampler {
 // sums and inside one chunk, and the row is read once more for the token's index among its equals.
 // A count can pass 16 bits where more than half of the row's tokens are equal; then the counts do not add up to
 // the tokens, and the row goes the other way.
+constexpr int kCountFrom = 40000;  // tokens of a row above which it is counted
 constexpr int kCountThreads = 1024, kChunks = 1024, kOrdered = 993;  // 497 chunks from +inf down to 0, 496 below
 struct CountSmem {
   uint32_t count[32768];   // patterns 2 i and 2 i + 1
@@ -1372,8 +1373,12 @@ cudaError_t launch_sample_t(cudaStream_t s, const SampleArgs& a) {
     return (size_t)((runs + nb - 1) / nb) * 16;
   };
   if constexpr (sizeof(T) == 2) {
-    // more rows than clusters of 8 can take at once: a block a row, by counting
-    if ((int64_t)a.rows * kMaxCluster > n_sm && a.vocab <= kMaxSlice) {
+    // Counting clears and adds up 65,536 counts a row, however short, and has an SM a row, so it is for long rows and
+    // many. fp16 without cuts / with top-p, us, counted and by bins: 128,256 tokens, 20 rows 33 and 27 / 34 and 37, 40 rows
+    // 33 and 39 / 34 and 49, 256 rows 65 and 133 / 68 and 158; 50,000 tokens, 40 rows 25 and 24 / 27 and 29, 256 rows 50 and
+    // 60 / 53 and 72; 32,000 tokens, 40 rows 23 and 18 / 24 and 23, 256 rows 45 and 40 / 48 and 51; 1,000 tokens,
+    // 40 rows 18 and 8 / 20 and 11, 256 rows 34 and 11 / 37 and 17.
+    if (a.vocab > kCountFrom && a.vocab <= kMaxSlice && (int64_t)a.rows * 4 > n_sm) {
       constexpr int smem = (int)std::max(sizeof(CountSmem), sizeof(SampleSmem<1>));
       e = cudaFuncSetAttribute(sample_counted_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return e;

@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import quantized_decode_step_gb300 as mag
-from tests.test_gpu_ops import ALL_KV, KV_NAMES, as_stored, check, half, make, reference, rows_of, sample_case
+from tests.test_gpu_ops import (ALL_KV, KV_NAMES, as_stored, check, extreme_rows, half, make, reference, rows_of,
+                                sample_case)
 
 pytestmark = pytest.mark.gpu
 
@@ -364,3 +365,81 @@ def test_sample_bins_as_wide_as_their_adds_allow():
     sample_case(x, u=u)
     sample_case(x, p=0.5, u=u)
     sample_case(x, k=131070, u=u)
+
+
+# ------------------------------------------------------------------------------------------------ rows that are counted by value
+COUNTED = [(39, 40001), (45, 65536), (160, 50021), (40, 131071)]  # fp16, many long rows
+EITHER = [(38, 131071), (160, 40000)]                             # their neighbours, which are not
+
+
+@pytest.mark.parametrize("rows,vocab", COUNTED + EITHER)
+def test_sample_counted_cuts(rows, vocab):
+    rng = np.random.default_rng(rows + vocab)
+    x = rows_of(rng, rows, vocab, np.float16)
+    sample_case(x, seed=1)
+    sample_case(x, t=0.9, k=5, seed=3)
+    sample_case(x, t=1.3, p=0.8, seed=4)
+    sample_case(x, m=0.05, seed=5)
+    sample_case(x, t=rng.uniform(0.3, 2, rows), k=rng.integers(0, vocab + 2, rows), p=rng.uniform(0, 1.1, rows),
+                m=rng.uniform(-0.1, 0.5, rows), seed=6)
+    sample_case(x, t=rng.uniform(0.3, 2, rows), k=rng.integers(400, 1100, rows), p=rng.uniform(0.5, 1.1, rows), seed=7)
+
+
+@pytest.mark.parametrize("rows,vocab", COUNTED)
+def test_sample_counted_crowds_and_ties(rows, vocab):
+    """Equal and nearly equal logits: cuts and draws inside them, by index."""
+    rng = np.random.default_rng(vocab)
+    flat = np.full((rows, vocab), 1.5, np.float16)
+    steps = (rng.integers(0, 4, (rows, vocab)) * 0.5).astype(np.float16)
+    peak = steps.copy()
+    peak[:, vocab // 3] = 9.0
+    for x in (flat, steps, peak):
+        sample_case(x, seed=1)
+        sample_case(x, k=vocab // 2, seed=2)
+        sample_case(x, t=2.0, p=0.3, m=0.4, seed=4)
+        sample_case(x, t=0.05, k=3000, m=0.9, seed=6)
+
+
+def test_sample_counted_more_equal_tokens_than_16_bits():
+    """Counts past 65,535, of even and odd patterns, at the top and below it: such a row is not counted."""
+    rng = np.random.default_rng(5)
+    x = rows_of(rng, 40, 131000, np.float16)
+    for r in range(40):
+        few = rng.permutation(131000)[:65536 + 1500 * r]
+        x[r, few] = np.array([0x3C00 + r % 2], np.uint16).view(np.float16)[0] * (1 if r % 3 else -1)
+    x[::5, 77] = 14.0
+    sample_case(x, t=0.8, seed=1)
+    sample_case(x, t=1.2, k=rng.integers(0, 131000, 40), p=rng.uniform(0.1, 1.1, 40), m=rng.uniform(-0.1, 0.2, 40), seed=2)
+
+
+def test_sample_counted_strides_and_masks():
+    rng = np.random.default_rng(9)
+    for ld in (41001, 41008, 41024):
+        x = rows_of(rng, 42, 41001, np.float16)
+        allowed = rng.random((42, 41001)) < np.tile(np.array([[1.0], [0.5], [0.01], [0.0], [0.9], [0.002]]), (7, 1))
+        allowed[4, np.argsort(-x[4].astype(np.float64))[:5]] = False
+        sample_case(x, t=0.8, k=[0, 3, 0, 4, 10, 0] * 7, p=0.9, allowed=allowed, ld=ld, seed=ld)
+        sample_case(x, t=0.8, m=[0, 0.1, 0, 0.9, 1e-3, 0] * 7, allowed=allowed, ld=ld, seed=ld)
+
+
+def test_sample_counted_extremes():
+    rng = np.random.default_rng(12)
+    x = rows_of(rng, 45, 40100, np.float16)
+    for at in range(0, 45, 9):
+        extreme_rows(x[at:at + 9], np.float16)
+    got, _ = sample_case(x, seed=3)
+    assert got[0] == got[1] == -1 and got[2] in (5, 17, 200)
+    for t in (0.0, float("nan"), 1e-30, 1e-6, 1e6, 1e30):
+        sample_case(x, t=t, seed=4)
+    for p in (0.0, 1e-9, 5.0):
+        sample_case(x, p=p, seed=5)
+    for m in (2.0, 1.0, 0.999, 1e-9):
+        sample_case(x, m=m, seed=6)
+    sample_case(x, k=2 ** 31 - 1, seed=8)
+    sample_case(x, k=1500, m=0.5, seed=9)
+    token, n = torch.full((45,), -7, dtype=torch.int32, device="cuda"), 40100
+    u = torch.tensor([math.nan, -1.0, 1.0, 2.0, math.inf] * 9, device="cuda")
+    mag.sample(torch.from_numpy(x).cuda(), 45, n, u, token, top_k=torch.full((45,), 1200, dtype=torch.int32, device="cuda"))
+    for r, t in enumerate(token.cpu().tolist()):
+        ok = np.flatnonzero(x[r] > -np.inf)
+        assert (t == -1) if len(ok) == 0 else t in ok[np.argsort(-x[r][ok].astype(np.float64), kind="stable")[:1200]]
