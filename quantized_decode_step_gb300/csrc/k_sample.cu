@@ -943,7 +943,8 @@ class Sampler {
 // sums and inside one chunk, and the row is read once more for the token's index among its equals.
 // A count can pass 16 bits where more than half of the row's tokens are equal; then the counts do not add up to
 // the tokens, and the row goes the other way.
-constexpr int kCountFrom = 40000;  // tokens of a row above which it is counted
+constexpr int kCountFrom = 40000;  // tokens of a row above which it may be counted
+constexpr int kListUpTo = 448;     // largest top-k of one that is not
 constexpr int kCountThreads = 1024, kChunks = 1024, kOrdered = 993;  // 497 chunks from +inf down to 0, 496 below
 struct CountSmem {
   uint32_t count[32768];   // patterns 2 i and 2 i + 1
@@ -1319,9 +1320,10 @@ class CountedRow {
 
 __global__ void __launch_bounds__(kCountThreads, 1) sample_counted_kernel(const __grid_constant__ SampleArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  // a row with a top-k that the partial maxima bring down to a list needs no count (256 rows of 128,256: 35 us, 57 counted)
+  // a row with a small top-k needs no count, since the partial maxima bring it down to a short list: 256 rows of 128,256, 51 us
+  // counted, listed 34 at k = 50, 43 at 200, 50 at 450, 55 at 512 (a longer sort), 74 at 1,024; of 50,000 and more the same order
   const int k = a.top_k ? a.top_k[blockIdx.x] : 0;
-  if ((k <= 0 || k > kCap / 2) && CountedRow(a, *reinterpret_cast<CountSmem*>(smem_raw)).run()) return;
+  if ((k <= 0 || k > kListUpTo) && CountedRow(a, *reinterpret_cast<CountSmem*>(smem_raw)).run()) return;
   __syncthreads();
   Sampler<__half, 1, kCountThreads, false>(a, *reinterpret_cast<SampleSmem<1>*>(smem_raw), nullptr).run();
 }
