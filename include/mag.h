@@ -296,13 +296,13 @@ mag_status mag_kv_export(mag_ctx* ctx, int32_t session, int32_t first, int32_t n
  * over the keys j <= p of a token at position p, and j > p - window when window > 0 (0: no window); k and v are the
  * fp16 values that mag_kv_read gives. q_dev is fp16 [rows][n_heads][head_dim] (already rotated), row stride ldq;
  * out_dev the same with row stride ldo; the two must not overlap. The sums, the softmax and its maximum are kept in
- * fp32; for the products with v its weights are rounded to fp16 (2^-11 of a weight, 2^-32 of the row's largest). Sessions of
- * up to 128 packed rows (tokens times n_heads / n_kv_heads) divide by the sum of the rounded weights, longer chunks by that of
- * the weights before the rounding: values that are all equal come back as they are from the one, to 2^-11 of themselves
- * from the other. A row's result does not depend on the other sessions of the call beyond how its keys are split over blocks.
- * The sessions' stored keys and values must be finite, those outside the window too (the product of 0 and an infinite
- * value is NaN); slots past a session's end may hold anything. scale must be finite, and below 2.3e38; so must
- * every scaled score be.
+ * fp32; for the products with v its weights are rounded to fp16 (2^-11 of a weight, 2^-25 of the row's largest).
+ * Sessions of up to 128 packed rows (tokens times n_heads / n_kv_heads) divide by the sum of the rounded weights,
+ * longer chunks by that of the weights before the rounding: values that are all equal come back as they are from
+ * the one, to 2^-11 of themselves from the other. A row's result does not depend on the other sessions of the call
+ * beyond how its keys are split over blocks. The sessions' stored keys and values must be finite, those outside the
+ * window too (the product of 0 and an infinite value is NaN); slots past a session's end may hold anything. scale
+ * must be finite, and below 2.3e38; so must every scaled score be.
  * Errors: INVALID_ARG (also a context's first call in a capture), OOM (the workspace), CUDA. */
 mag_status mag_attend(mag_ctx* ctx, int32_t layer, int32_t n_sessions, const int32_t* session_ids_host,
                       const int32_t* n_tokens_host, const void* q_dev, int64_t ldq, void* out_dev, int64_t ldo,
@@ -329,9 +329,10 @@ typedef struct mag_sample_params {
  *   token is the first whose running sum of w exceeds u times the prefix's sum.
  * Sums are exact in integers (w in units of 2^-40), so a result depends on nothing but its row. token_dev[row] is
  * the token's index, -1 for a row with no token to draw (none allowed, or every logit NaN or -inf; those are never
- * drawn); prob_dev[row] (may be null) its share of the kept w, to 2^-23 of itself however small, NaN for a row without a
- * token. Infinite logits share all the weight. A uniform number below 0 or NaN counts as 0, one of 1 or more takes the prefix's last
- * token. p may be null (temperature 1, no cuts). Arrays are aligned to their elements.
+ * drawn); prob_dev[row] (may be null) its share of the kept w, to 2^-23 of itself however small, NaN for a row without
+ * a token. Infinite logits share all the weight, fp32 ones further below the largest than fp32 holds have none. A uniform
+ * number below 0 or NaN counts as 0, one of 1 or more takes the prefix's last token. p may be null (temperature 1,
+ * no cuts). Arrays are aligned to their elements.
  * Errors: INVALID_ARG, UNSUPPORTED (vocab above 540,672 in fp16, 270,336 in fp32), CUDA. */
 mag_status mag_sample(const void* logits_dev, int32_t logits_type, int32_t rows, int32_t vocab, int64_t ld,
                       const mag_sample_params* p, const float* uniform_dev, int32_t* token_dev, float* prob_dev,

@@ -6,7 +6,7 @@
 
 #define MAG_MAX_BATCH 16
 
-// Error-word bits of the device-side checks (the waits that give up use bits 2-8): a pool block id read
+// Error-word bits of the device-side checks (the waits that give up use bits 2-9): a pool block id read
 // from a block table outside the pool (the id is not used), and a changed arena canary band (bit 16 + i:
 // arena tensor i).
 constexpr uint32_t kErrBounds = 2048u;

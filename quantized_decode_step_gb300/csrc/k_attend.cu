@@ -189,8 +189,8 @@ __device__ __forceinline__ uint32_t v_pair(const uint32_t (&a)[Raw<D, KV>::VW], 
 }
 
 // Warps of a block, one block per SM: as many as the registers of a warp's operands leave room for. FP16 holds 64
-// registers of a pool block (in flight or in use), and 8 rows of o and Q another 48; INT8 and INT4, whose bound
-// is the instructions of their expansion, need warps more than bytes in flight.
+// registers of a pool block (in flight or in use), and 8 rows of o and Q another 48. INT8 and INT4 are bound by what these
+// few warps hide: issue 48%, a quarter to a third of a warp's waits for loads, a quarter for fixed latencies.
 template <int D, int KV, int NT>
 constexpr int few_warps() {
   return D == 64 ? (KV == 0 && NT == 2 ? 12 : 16) : (KV == 0 ? (NT == 1 ? 12 : 8) : (NT == 1 ? 16 : 12));

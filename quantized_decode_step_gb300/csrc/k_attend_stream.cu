@@ -3,13 +3,13 @@
 //
 //   o_t = sum_j softmax_j(scale q_t . k_j) v_j   over the keys j <= p_t, and j > p_t - window if there is one.
 //
-// What bounds it: K and V are read once for all rows, so with one tile of rows the loads and the chain from a step's
-// scores to its products, about 1.5 us a step of 128 keys in each stream. A 128-row MMA tile is mostly padding with few rows,
-// but the tensor core has the time, and everything that costs instructions is done once: the expansion of INT8 and INT4
-// by eight warps of their own, the softmax by the one warp per stream and 32 rows that has any. 20 rows over 20,000
-// FP16 keys, 8 KV heads of 128: 68 us in 16-row tiles of the register kernel, 30 here; 128 rows of INT4 80 against 34. For up
-// to 16 rows the register kernel reads the keys once as well and is faster (16 rows over 16 sessions' INT8 keys 59 us
-// against 156).
+// What bounds it: K and V are read once for all rows, so the loads, and the chain from a step's scores to its products. A
+// block takes a step of 128 keys (of either stream) in 1.8 us of FP16, 0.8 of the copy rate over 152 blocks, and in 2.25
+// of INT8 and 1.75 of INT4, where it is the chain: issue 36%, the warps' waits mostly loads (28%) and instruction
+// fetch (18%). A call takes about 12 us besides, for its start and the merge. A 128-row MMA tile is mostly padding with few
+// rows, but the tensor core has the time, and everything that costs instructions is done once: the expansion of INT8 and
+// INT4 by eight warps of their own, the softmax by the one warp per stream and 32 rows that has any. Up to 16 rows the
+// register kernel reads the keys once as well and is faster; beyond, and from where on the two-tile kernel is: ops.cu.
 //
 // Even and odd steps of 128 keys are two streams with a maximum, a sum and an o each, so that one's softmax runs while
 // the tensor core has the other's products; they are joined at the end, in tensor memory. Roles, the softmax's base and

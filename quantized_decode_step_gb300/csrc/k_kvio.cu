@@ -236,8 +236,8 @@ cudaError_t launch_kv_read(const Launch& L, const KvReadArgs& a, int n_layers) {
   if (a.n_blocks < 1 || n_layers < 1 || n_layers > 65535 || a.rows.n_seg < 1 || a.rows.n_seg > MAG_MAX_BATCH)
     return cudaErrorInvalidValue;
   const dim3 grid(a.n_blocks, 2, n_layers);
-  return launch_kernel(L, a.pool.kv_dtype == 0 ? kv_read_kernel<0> : (a.pool.kv_dtype == 1 ? kv_read_kernel<1> : kv_read_kernel<2>),
-                       grid, dim3(kIoThreads), 0, a);
+  auto kernel = a.pool.kv_dtype == 0 ? kv_read_kernel<0> : (a.pool.kv_dtype == 1 ? kv_read_kernel<1> : kv_read_kernel<2>);
+  return launch_kernel(L, kernel, grid, dim3(kIoThreads), 0, a);
 }
 
 }  // namespace mag

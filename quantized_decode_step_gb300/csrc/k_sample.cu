@@ -18,10 +18,11 @@
 // arithmetic only where u falls within about 1e-9 / sqrt(tokens) of a border.
 //
 // What bounds it: the logits are read once from HBM (256 rows of 128,256 in fp16: 10 us), so with few rows the
-// latency of the passes between cluster barriers, with many the instructions and shared-memory adds of a token:
-// about 7 and 1 to count it, 30 and 2 or 3 for its weight. With few rows a cluster of blocks shares a row, each
-// with its slice in shared memory, as many blocks as the row count leaves SMs for; with many a block has a row and later
-// passes read it from L2: two blocks an SM, or one where long fp16 rows are counted by value (132 KB of counts).
+// latency of the passes between cluster barriers, with many the passes' waits for the row from L2 and the
+// instructions and shared-memory adds of a token: about 7 and 1 to count it, 30 and 2 or 3 for its weight. With few
+// rows a cluster of blocks shares a row, each with its slice in shared memory, as many blocks as the row count
+// leaves SMs for; with many a block has a row and later passes read it from L2: two blocks an SM, or one where long
+// fp16 rows are counted by value (132 KB of counts).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -1320,8 +1321,8 @@ class CountedRow {
 
 __global__ void __launch_bounds__(kCountThreads, 1) sample_counted_kernel(const __grid_constant__ SampleArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  // a row with a small top-k needs no count, since the partial maxima bring it down to a short list: 256 rows of 128,256, 51 us
-  // counted, listed 34 at k = 50, 43 at 200, 50 at 450, 55 at 512 (a longer sort), 74 at 1,024; of 50,000 and more the same order
+  // a row with a small top-k needs no count, since the partial maxima bring it down to a short list: 256 rows of 128,256,
+  // 51 us counted, listed 34 at k = 50, 43 at 200, 50 at 450, 55 at 512 (a longer sort), 74 at 1,024; others alike
   const int k = a.top_k ? a.top_k[blockIdx.x] : 0;
   if ((k <= 0 || k > kListUpTo) && CountedRow(a, *reinterpret_cast<CountSmem*>(smem_raw)).run()) return;
   __syncthreads();

@@ -308,7 +308,7 @@ cudaError_t launch_kv_read(const Launch& L, const KvReadArgs& a, int n_layers);
 // Causal grouped-query attention of the sessions' newest tokens over the pool. The G query heads of a KV head and
 // the tokens of a session are packed into rows, row t G + g, cut into tiles; a unit is one (session, KV head, tile)
 // over its keys in steps. The units' steps, in order, are dealt out to the blocks in shares; blocks that share a unit
-// leave (m, l, o) in the workspace for the last of them to merge.
+// leave (m, l, o) in the workspace, which the last of them puts together (few rows), or a second launch.
 struct AttendSeg {
   int32_t row0, n_tok, pos0, sess;  // as KvSeg
   int32_t unit0, n_tiles;           // units of this session: unit0 + head * n_tiles + tile
@@ -322,7 +322,7 @@ struct AttendArgs {
   int32_t window;      // 0: every key up to the token's own
   float scale_log2;    // scale * log2(e)
   float* part;         // o of cut pieces, two a block, fp32
-  float* part_ml;      // few rows: their running maxima (log2 units) and sums
+  float* part_ml;      // few rows: their running maxima (log2 units) and sums; the others keep theirs, unscaled, behind o
   uint32_t* arrivals;  // zero between launches
   int32_t n_seg, n_units;
   AttendSeg seg[MAG_MAX_BATCH];

@@ -96,10 +96,16 @@ static mag_status attend_workspace(mag_ctx* c) {
   return MAG_OK;
 }
 
-// Which kernel a session goes to, by its packed rows (tokens times query heads per KV head): up to kFewRows to the
-// register kernel (one of its tiles; with the streaming kernel 16 sessions' single tokens over INT8 keys take 156 us for
-// 59), up to kStreamRows (one tile) to the streaming one (20 rows over 20,000 FP16 keys: 30 us for the register
-// kernel's 68), others to the two-tile one.
+// Which kernel a session goes to, by its packed rows (tokens times query heads per KV head). Up to kFewRows, one
+// tile of the register kernel, that one (us, register and streaming; 32 heads over 8 KV heads of 128): 16 rows on
+// 20,000 keys, one session FP16 24 and 27, INT8 22 and 32, INT4 24 and 28; 16 sessions 217 and 237, 169 and 297,
+// 171 and 228. Up to kStreamRows, one tile of the streaming kernel, that one: 20 rows, one session 29 and 27, 28
+// and 32, 30 and 28; 16 sessions 421 and 238, 323 and 296, 324 and 228; of 2,000 keys 59 and 38, 46 and 40, 49 and
+// 33 (one INT8 session, and one or four short ones, are faster in registers, by a tenth). So a fifth draft token
+// costs 16 INT8 sessions 169 -> 296, and two register tiles would cost them more. Others to the two-tile one
+// (streaming and two-tile: 256 rows on 20,000 keys 41 and 32, 49 and 40, 42 and 38; on 800 keys 12 and 15, 14 and
+// 17, 13 and 17; 2,048 rows on 800 26 and 26, 31 and 31, 27 and 31; 8,192 on 2,000 166 and 108, 240 and 141, 211
+// and 137). The kernels of one call run one after another.
 constexpr int kFewRows = 16, kStreamRows = 128;
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -257,7 +263,8 @@ mag_status mag_attend(mag_ctx* c, int32_t layer, int32_t n, const int32_t* sids,
   mag_status st = op_rows(c, "attend", layer, n, sids, ntok, rows);
   if (st != MAG_OK) return st;
   if (window < 0) return fail(c, MAG_ERR_INVALID_ARG, "attend: window %d", window);
-  if (!std::isfinite(scale * kLog2e)) return fail(c, MAG_ERR_INVALID_ARG, "attend: the scale, or its log2(e)-fold, is not finite");
+  if (!std::isfinite(scale * kLog2e))
+    return fail(c, MAG_ERR_INVALID_ARG, "attend: the scale, or its log2(e)-fold, is not finite");
   if (rows.n_rows == 0) return MAG_OK;
   if ((st = op_buffer(c, "attend", "q", q, ldq, (int64_t)c->Hq * c->d)) != MAG_OK) return st;
   if ((st = op_buffer(c, "attend", "out", out, ldo, (int64_t)c->Hq * c->d)) != MAG_OK) return st;
